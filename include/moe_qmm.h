@@ -309,6 +309,102 @@ moe_status moe_qmm_id_w4a4(const void *x, const uint32_t *ids, const void *packe
                            moe_dtype x_dtype, moe_dtype out_dtype, void *workspace, size_t workspace_bytes,
                            moe_stream_t stream, moe_path path);
 
+/* ------------------------------------------------- the layer around the product
+ *
+ * What a serving program runs around moe_qmm_id in an expert layer: the router's
+ * choice, the gated expert MLP with its sum over a token's experts, and that sum
+ * alone. (The pages run these steps outside the code they show; the definitions
+ * are written out here.) The conventions above hold: device pointers, work on
+ * `stream`, no synchronisation, no allocation.
+ */
+
+typedef enum {
+    MOE_SCORE_SOFTMAX = 0, /* p[e] = exp(l[e] - max l) / sum_j exp(l[j] - max l) */
+    MOE_SCORE_SIGMOID = 1  /* p[e] = 1 / (1 + exp(-l[e]))                         */
+} moe_score;
+
+/* Largest top_k of moe_gate_topk. */
+#define MOE_GATE_MAX_TOPK 32u
+
+/*
+ * moe_gate_topk -- the experts of each token and their weights from the router's
+ * logits.
+ *   logits       [m, num_experts] of logits_dtype (element-aligned).
+ *   select_bias  [num_experts] f32, or NULL: added to the scores for the choice
+ *                alone, not in the weights. With MOE_SCORE_SIGMOID only.
+ *   ids          [m, top_k] u32: the chosen experts, best first; ties go to the
+ *                lowest expert.
+ *   weights      [m, top_k] f32: scale * p[e] of the chosen, divided by the sum of
+ *                the top_k chosen p where renormalize is non-zero.
+ * The choice is by the logits without a bias (both scores are monotonic; exact),
+ * and by p + bias in 64 bits with one. A logit of -inf masks its expert: it is
+ * chosen after every other and has weight 0; a token whose logits are all -inf has
+ * weights 0. A NaN logit ranks below -inf and makes the weights that it enters NaN,
+ * as a logit of +inf does under softmax.
+ * MOE_ERR_INVALID_ARGUMENT: zero sizes, top_k > num_experts, unknown types, NULL
+ * or misaligned arrays, a bias with softmax. MOE_ERR_UNSUPPORTED: num_experts >
+ * MOE_ROUTE_MAX_EXPERTS, top_k > MOE_GATE_MAX_TOPK, m >= 2^31.
+ */
+moe_status moe_gate_topk(const void *logits, const float *select_bias, uint32_t *ids, float *weights, uint32_t m,
+                         uint32_t num_experts, uint32_t top_k, moe_dtype logits_dtype, moe_score score,
+                         int renormalize, float scale, moe_stream_t stream);
+
+/*
+ * moe_combine -- the weighted sum of a token's rows:
+ *     out[t][c] = residual[t][c] + sum_s weights[t][s] * z[t][s][c]
+ *   z         [m, n_expert_used, n] of z_dtype, for example moe_qmm_id's output.
+ *   weights   [m, n_expert_used] f32.
+ *   ids       [m, n_expert_used] u32, or NULL: pairs whose id is >= num_experts are
+ *             left out (their rows of z and their weights are not read into the sum).
+ *   residual  [m, n] of out_dtype, or NULL; may be out itself.
+ *   out       [m, n] of out_dtype; must not overlap z.
+ * The sum is formed in f32 in slot order, the residual added last, and rounded
+ * once. Arrays are element-aligned (16-byte boundaries are faster).
+ */
+moe_status moe_combine(const void *z, const float *weights, const uint32_t *ids, const void *residual, void *out,
+                       uint32_t m, uint32_t n_expert_used, uint32_t n, uint32_t num_experts, moe_dtype z_dtype,
+                       moe_dtype out_dtype, moe_stream_t stream);
+
+/* One projection's weights of all experts, as moe_qmm_id takes them. */
+typedef struct {
+    const void *packed, *scales, *aux; /* device arrays, laid out as for moe_qmm_id       */
+    const void *bias;                  /* [num_experts, n] of bias_dtype, or NULL         */
+    uint32_t group_size, bits;
+    moe_fmt fmt;
+    moe_dtype bias_dtype;
+} moe_expert_weights;
+
+/*
+ * moe_mlp -- the gated expert MLP of a layer and the sum over a token's experts:
+ *     h[t][s] = act(G_e x[t] + bg_e) * (U_e x[t] + bu_e),   e = ids[t][s]
+ *     out[t]  = residual[t] + sum_s weights[t][s] * (D_e h[t][s] + bd_e)
+ *   x         [m, hidden] of x_dtype.
+ *   ids       [m, n_expert_used] u32; pairs with an id >= num_experts are left out
+ *             and set the error word's bit, as in moe_qmm_id.
+ *   weights   [m, n_expert_used] f32 (moe_gate_topk's).
+ *   gate_up   the gate and up projections, 2 * inter rows of hidden values an
+ *             expert: rows [0, inter) gate, [inter, 2 inter) up (moe_qmm_id_glu).
+ *   down      the down projection, hidden rows of inter values an expert.
+ *   residual  [m, hidden] of out_dtype, or NULL; may be out itself.
+ *   out       [m, hidden] of out_dtype; must not overlap x.
+ *   workspace of moe_mlp_workspace_bytes for these sizes (or for a larger m),
+ *             16-byte aligned, its first 4 bytes zero before the first use: the
+ *             device error word that moe_qmm_id_poll_error reads and clears. Calls
+ *             that share it must be ordered on the GPU.
+ *   path      MOE_PATH_AUTO; MOE_PATH_DECODE and MOE_PATH_GROUPED make both products
+ *             take that path, with moe_qmm_id_path's errors. No launch flags.
+ * The two products' formats may differ. h is held in bf16 for bf16 x and in f32
+ * otherwise; the products and the sum are accumulated in f32 and out is rounded
+ * once. Errors as moe_qmm_id_glu and moe_combine.
+ */
+size_t moe_mlp_workspace_bytes(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t n_expert_used,
+                               uint32_t num_experts, moe_dtype x_dtype);
+moe_status moe_mlp(const void *x, const uint32_t *ids, const float *weights, const moe_expert_weights *gate_up,
+                   const moe_expert_weights *down, const void *residual, void *out, uint32_t m, uint32_t hidden,
+                   uint32_t inter, uint32_t n_expert_used, uint32_t num_experts, moe_dtype x_dtype,
+                   moe_dtype out_dtype, moe_act act, void *workspace, size_t workspace_bytes, moe_stream_t stream,
+                   moe_path path);
+
 /* Bytes of one packed weight row (mlx-native quantized_matmul_id.rs,
  * expert_weight_bytes per row): AFFINE 4/8 and CODEBOOK ceil(k / (32/bits)) * 4,
  * AFFINE 6 ceil(k / 4) * 3, NVFP4 k / 2. Returns 0 for an invalid (fmt, bits). */

@@ -15,6 +15,7 @@ tensor is not on a CUDA device, calls raise.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -29,6 +30,9 @@ ACT_SILU, ACT_GELU_TANH, ACT_GELU_ERF = 0, 1, 2
 # launch flags OR-ed into the path argument (programmatic dependent launch)
 LAUNCH_PDL, LAUNCH_EARLY_WEIGHTS = 0x100, 0x200
 _LAUNCH = {None: 0, "pdl": LAUNCH_PDL, "early_weights": LAUNCH_PDL | LAUNCH_EARLY_WEIGHTS}
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+_SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
+GATE_MAX_TOPK, ROUTE_MAX_EXPERTS = 32, 1024
 ACTS = {"silu": ACT_SILU, "gelu_tanh": ACT_GELU_TANH, "gelu_erf": ACT_GELU_ERF}
 
 MOE_OK = 0
@@ -91,6 +95,14 @@ def lib() -> ctypes.CDLL:
         L.moe_qmm_id_route.restype = i32
         L.moe_qmm_id_poll_error.argtypes = [vp, vp]
         L.moe_qmm_id_poll_error.restype = i32
+        L.moe_gate_topk.argtypes = [vp] * 4 + [u32] * 3 + [i32] * 3 + [ctypes.c_float, vp]
+        L.moe_gate_topk.restype = i32
+        L.moe_combine.argtypes = [vp] * 5 + [u32] * 4 + [i32, i32, vp]
+        L.moe_combine.restype = i32
+        L.moe_mlp.argtypes = [vp] * 7 + [u32] * 5 + [i32] * 3 + [vp, sz, vp, i32]
+        L.moe_mlp.restype = i32
+        L.moe_mlp_workspace_bytes.argtypes = [u32] * 5 + [i32]
+        L.moe_mlp_workspace_bytes.restype = sz
         L.moe_status_str.argtypes = [i32]
         L.moe_status_str.restype = ctypes.c_char_p
         _lib = L
@@ -439,3 +451,222 @@ def qmm_id_w4a4(x: torch.Tensor, ids: torch.Tensor, packed: torch.Tensor, scales
     if st != MOE_OK:
         raise MoeError(st, "moe_qmm_id_w4a4")
     return out
+
+
+# ----------------------------------------------------------- the layer around it
+
+
+def _on_device(device):
+    """The tensors' device made current for a launch (their stream belongs to it)."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _want(t, what: str, shape: tuple, device, dtypes):
+    """One tensor argument's checks: a contiguous CUDA tensor on `device` of one of
+    the types and exactly this shape."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a torch.Tensor")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{what} must be on {device}, got {t.device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what} must be of {sorted(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+
+
+_IDS = (torch.int32, torch.uint32)
+_F32 = (torch.float32,)
+
+
+def gate_topk(logits: torch.Tensor, top_k: int, *, score: str = "softmax",
+              select_bias: torch.Tensor | None = None, renormalize: bool = True, scale: float = 1.0,
+              ids: torch.Tensor | None = None, weights: torch.Tensor | None = None):
+    """moe_gate_topk: the top_k experts of each token and their weights from router
+    logits [m, num_experts] (f32 / bf16 / f16), on the current CUDA stream. Returns
+    (ids [m, top_k] int32, weights [m, top_k] f32), best first, ties to the lowest
+    expert; both may be given to be written. score "softmax" or "sigmoid"; select_bias
+    [num_experts] f32 (sigmoid only) is added for the choice alone; renormalize
+    divides the weights by their sum, scale multiplies them.
+    """
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("gate_topk: logits must be a [m, num_experts] tensor")
+    if not logits.is_cuda or not logits.is_contiguous() or logits.dtype not in _TORCH_DT:
+        raise ValueError("gate_topk: logits must be a contiguous f32/bf16/f16 CUDA tensor")
+    m, E = logits.shape
+    if score not in _SCORES:
+        raise ValueError(f"gate_topk: unknown score {score!r} (one of {sorted(_SCORES)})")
+    if not 1 <= top_k <= E:
+        raise ValueError(f"gate_topk: top_k must be 1..num_experts, got {top_k} of {E}")
+    device = logits.device
+    if select_bias is not None:
+        if score != "sigmoid":
+            raise ValueError("gate_topk: a selection bias goes with sigmoid scores")
+        _want(select_bias, "gate_topk: select_bias", (E,), device, _F32)
+    if ids is None:
+        ids = torch.empty((m, top_k), dtype=torch.int32, device=device)
+    else:
+        _want(ids, "gate_topk: ids", (m, top_k), device, _IDS)
+    if weights is None:
+        weights = torch.empty((m, top_k), dtype=torch.float32, device=device)
+    else:
+        _want(weights, "gate_topk: weights", (m, top_k), device, _F32)
+    if m == 0:
+        return ids, weights
+    with _on_device(device):
+        st = lib().moe_gate_topk(logits.data_ptr(), select_bias.data_ptr() if select_bias is not None else None,
+                                 ids.data_ptr(), weights.data_ptr(), m, E, top_k, _TORCH_DT[logits.dtype],
+                                 _SCORES[score], 1 if renormalize else 0, scale, _stream_ptr(device))
+    if st != MOE_OK:
+        raise MoeError(st, "moe_gate_topk")
+    return ids, weights
+
+
+def combine(z: torch.Tensor, weights: torch.Tensor, *, ids: torch.Tensor | None = None,
+            num_experts: int | None = None, residual: torch.Tensor | None = None,
+            out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """moe_combine: out[t] = residual[t] + sum_s weights[t, s] * z[t, s], for z
+    [m, n_expert_used, n] (f32 / bf16 / f16, for example qmm_id's output) and weights
+    [m, n_expert_used] f32. With ids and num_experts, pairs whose id is out of range
+    are left out. out (or out_dtype; default z's type) and residual [m, n] share one
+    type; residual may be out itself.
+    """
+    if not isinstance(z, torch.Tensor) or z.dim() != 3:
+        raise ValueError("combine: z must be a [m, n_expert_used, n] tensor")
+    if not z.is_cuda or not z.is_contiguous() or z.dtype not in _TORCH_DT:
+        raise ValueError("combine: z must be a contiguous f32/bf16/f16 CUDA tensor")
+    m, S, n = z.shape
+    device = z.device
+    _want(weights, "combine: weights", (m, S), device, _F32)
+    if (ids is None) != (num_experts is None):
+        raise ValueError("combine: ids and num_experts go together")
+    if ids is not None:
+        _want(ids, "combine: ids", (m, S), device, _IDS)
+        if num_experts <= 0:
+            raise ValueError("combine: num_experts must be > 0")
+    if out is None:
+        dt = out_dtype or (residual.dtype if residual is not None else z.dtype)
+        if dt not in _TORCH_DT:
+            raise ValueError(f"combine: unsupported output dtype {dt}")
+        out = torch.empty((m, n), dtype=dt, device=device)
+    else:
+        _want(out, "combine: out", (m, n), device, _TORCH_DT)
+    if residual is not None:
+        _want(residual, "combine: residual", (m, n), device, (out.dtype,))
+    if m == 0:
+        return out
+    if S == 0 or n == 0:
+        raise ValueError("combine: n_expert_used and n must be > 0")
+    with _on_device(device):
+        st = lib().moe_combine(z.data_ptr(), weights.data_ptr(), ids.data_ptr() if ids is not None else None,
+                               residual.data_ptr() if residual is not None else None, out.data_ptr(), m, S, n,
+                               num_experts or 0, _TORCH_DT[z.dtype], _TORCH_DT[out.dtype], _stream_ptr(device))
+    if st != MOE_OK:
+        raise MoeError(st, "moe_combine")
+    return out
+
+
+class _WeightsStruct(ctypes.Structure):  # moe_expert_weights
+    _fields_ = [("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("aux", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("group_size", ctypes.c_uint32), ("bits", ctypes.c_uint32),
+                ("fmt", ctypes.c_int), ("bias_dtype", ctypes.c_int)]
+
+
+class ExpertWeights:
+    """One projection's weights of all experts (moe_expert_weights): packed, scales and
+    aux as qmm_id takes them, their format, and an optional bias [num_experts, n]."""
+
+    def __init__(self, packed: torch.Tensor, scales: torch.Tensor, aux: torch.Tensor, *, fmt: int, bits: int,
+                 group_size: int, bias: torch.Tensor | None = None):
+        self.packed, self.scales, self.aux, self.bias = packed, scales, aux, bias
+        self.fmt, self.bits, self.group_size = fmt, bits, group_size
+
+    def _struct(self) -> _WeightsStruct:
+        b = self.bias
+        return _WeightsStruct(self.packed.data_ptr(), self.scales.data_ptr(), self.aux.data_ptr(),
+                              b.data_ptr() if b is not None else None, self.group_size, self.bits, self.fmt,
+                              _TORCH_DT[b.dtype] if b is not None else 0)
+
+
+class MoeMlp:
+    """moe_mlp: a layer's gated expert MLP and the sum over a token's experts, with its
+    weights, sizes, types and workspace bound once.
+
+        layer = MoeMlp(ExpertWeights(...), ExpertWeights(...), hidden=2816, inter=704, num_experts=128,
+                       n_expert_used=8, max_tokens=256, x_dtype=torch.bfloat16, out_dtype=torch.bfloat16)
+        ids, weights = gate_topk(logits, 8)
+        out = layer(x, ids, weights, residual=x)      # [m, hidden], on the current stream
+
+    gate_up holds 2 * inter rows an expert (gate, then up), down hidden rows. A call
+    takes 1 .. max_tokens tokens. The workspace belongs to the layer: calls of one
+    layer object must be ordered on the GPU (one stream, or events), captured ones
+    included; poll_error(layer.workspace) reports ids out of range. path as qmm_id.
+    """
+
+    def __init__(self, gate_up: ExpertWeights, down: ExpertWeights, *, hidden: int, inter: int, num_experts: int,
+                 n_expert_used: int, max_tokens: int, x_dtype: torch.dtype = torch.bfloat16,
+                 out_dtype: torch.dtype | None = None, act: str = "silu", workspace: torch.Tensor | None = None,
+                 path: str = "auto"):
+        out_dtype = out_dtype or x_dtype
+        if min(hidden, inter, num_experts, n_expert_used, max_tokens) <= 0:
+            raise ValueError("MoeMlp: sizes must be > 0")
+        if x_dtype not in _TORCH_DT or out_dtype not in _TORCH_DT:
+            raise ValueError("MoeMlp: x and out are f32, bf16 or f16")
+        if path not in _PATHS:
+            raise ValueError(f"MoeMlp: unknown path {path!r}")
+        if act not in ACTS:
+            raise ValueError(f"MoeMlp: unknown activation {act!r} (one of {sorted(ACTS)})")
+        device = gate_up.packed.device
+        # each projection's arrays, by qmm_id's own checks, on placeholders for x and ids
+        ids0 = torch.empty((1, 1), dtype=torch.int32, device=device)
+        for w, k, n, a in ((gate_up, hidden, 2 * inter, act), (down, inter, hidden, None)):
+            _validate_only(torch.empty((1, k), dtype=torch.float32, device=device), ids0, w.packed, w.scales,
+                           w.aux, n=n, group_size=w.group_size, bits=w.bits, fmt=w.fmt, num_experts=num_experts,
+                           out=None, expert_bias=w.bias, act=a, launch=None)
+        need = int(lib().moe_mlp_workspace_bytes(max_tokens, hidden, inter, n_expert_used, num_experts,
+                                                 _TORCH_DT[x_dtype]))
+        if need == 0:
+            raise ValueError("MoeMlp: sizes overflow the workspace layout")
+        if workspace is None:
+            workspace = torch.zeros(need, dtype=torch.uint8, device=device)
+        else:
+            _check_dev(workspace, "workspace", device)
+            if _nbytes(workspace) < need:
+                raise ValueError(f"MoeMlp: workspace too small: {need} bytes needed, got {_nbytes(workspace)}")
+        self.workspace, self.device, self.path = workspace, device, path
+        self.hidden, self.n_expert_used, self.max_tokens = hidden, n_expert_used, max_tokens
+        self.x_dtype, self.out_dtype = x_dtype, out_dtype
+        self._weights = (gate_up, down)  # keeps the arrays alive
+        self._structs = (gate_up._struct(), down._struct())
+        self._call = lib().moe_mlp
+        self._ptrs = tuple(ctypes.addressof(w) for w in self._structs)
+        self._bound = (hidden, inter, n_expert_used, num_experts, _TORCH_DT[x_dtype], _TORCH_DT[out_dtype],
+                       ACTS[act], workspace.data_ptr(), _nbytes(workspace))
+
+    def __call__(self, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                 residual: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+        """x [m, hidden], ids [m, n_expert_used] (int32 / uint32), weights [m, n_expert_used]
+        f32, residual [m, hidden] of the output type (may be out) -> out [m, hidden]."""
+        device, m = self.device, x.shape[0]
+        if m == 0 or m > self.max_tokens:
+            raise ValueError(f"MoeMlp: 1 to {self.max_tokens} tokens a call, got {m}")
+        _want(x, "MoeMlp: x", (m, self.hidden), device, (self.x_dtype,))
+        _want(ids, "MoeMlp: ids", (m, self.n_expert_used), device, _IDS)
+        _want(weights, "MoeMlp: weights", (m, self.n_expert_used), device, _F32)
+        if out is None:
+            out = torch.empty((m, self.hidden), dtype=self.out_dtype, device=device)
+        else:
+            _want(out, "MoeMlp: out", (m, self.hidden), device, (self.out_dtype,))
+        r = None
+        if residual is not None:
+            _want(residual, "MoeMlp: residual", (m, self.hidden), device, (self.out_dtype,))
+            r = residual.data_ptr()
+        hidden, inter, S, E, xd, od, act, ws, nbytes = self._bound
+        with _on_device(device):
+            st = self._call(x.data_ptr(), ids.data_ptr(), weights.data_ptr(), self._ptrs[0], self._ptrs[1], r,
+                            out.data_ptr(), m, hidden, inter, S, E, xd, od, act, ws, nbytes, _stream_ptr(device),
+                            _PATHS[self.path])
+        if st != MOE_OK:
+            raise MoeError(st, "moe_mlp")
+        return out

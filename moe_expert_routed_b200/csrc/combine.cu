@@ -1,0 +1,122 @@
+// combine.cu -- the weighted sum of a token's rows (include/moe_qmm.h, moe_combine):
+//   out[t][c] = residual[t][c] + sum_s weights[t][s] * z[t][s][c]
+// in one pass over z. Bound by memory: every byte of z is read once, out is
+// written once. A thread owns VEC neighbouring columns of one token and walks the
+// slots in order, so the sum (fp32) has one order and no atomics; the residual is
+// added last, before the only rounding.
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int COMBINE_THREADS = 256;
+
+struct CombineParams {
+    const void *z;
+    const float *w;
+    const uint32_t *ids;
+    const void *residual;
+    void *out;
+    uint64_t total;  // m * (n / VEC)
+    uint32_t S, n, E;
+};
+
+template <typename T> struct Cvt;
+template <> struct Cvt<float> {
+    static __device__ __forceinline__ float to(float v) { return v; }
+    static __device__ __forceinline__ float from(float v) { return v; }
+};
+template <> struct Cvt<__nv_bfloat16> {
+    static __device__ __forceinline__ float to(__nv_bfloat16 v) { return __bfloat162float(v); }
+    static __device__ __forceinline__ __nv_bfloat16 from(float v) { return __float2bfloat16_rn(v); }
+};
+template <> struct Cvt<__half> {
+    static __device__ __forceinline__ float to(__half v) { return __half2float(v); }
+    static __device__ __forceinline__ __half from(float v) { return __float2half_rn(v); }
+};
+
+template <typename T, int N> struct alignas(sizeof(T) * N) Pack { T v[N]; };
+
+template <typename TZ, typename TO, int VEC>
+__global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(const CombineParams P) {
+    const uint32_t nv = P.n / VEC;
+    for (uint64_t i = (uint64_t)blockIdx.x * COMBINE_THREADS + threadIdx.x; i < P.total;
+         i += (uint64_t)gridDim.x * COMBINE_THREADS) {
+        const uint64_t t = i / nv;
+        const uint32_t c = (uint32_t)(i - t * nv);
+        const Pack<TZ, VEC> *z = (const Pack<TZ, VEC> *)P.z + t * P.S * nv + c;
+        float acc[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; j++) acc[j] = 0.f;
+#pragma unroll 4
+        for (uint32_t s = 0; s < P.S; s++) {
+            if (P.ids && __ldg(P.ids + t * P.S + s) >= P.E) continue;
+            const float w = __ldg(P.w + t * P.S + s);
+            const Pack<TZ, VEC> v = z[(size_t)s * nv];
+#pragma unroll
+            for (int j = 0; j < VEC; j++) acc[j] = fmaf(w, Cvt<TZ>::to(v.v[j]), acc[j]);
+        }
+        Pack<TO, VEC> o;
+        if (P.residual) {
+            const Pack<TO, VEC> r = ((const Pack<TO, VEC> *)P.residual)[i];
+#pragma unroll
+            for (int j = 0; j < VEC; j++) acc[j] += Cvt<TO>::to(r.v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; j++) o.v[j] = Cvt<TO>::from(acc[j]);
+        ((Pack<TO, VEC> *)P.out)[i] = o;
+    }
+}
+
+template <typename TZ, typename TO>
+cudaError_t launch_t(CombineParams P, uint64_t m, cudaStream_t st) {
+    // wide accesses where rows start and end on their boundaries, single elements elsewhere
+    constexpr int W = 4;
+    const uintptr_t za = (uintptr_t)P.z, oa = (uintptr_t)P.out | (uintptr_t)P.residual;
+    const bool wide = P.n % W == 0 && za % (W * sizeof(TZ)) == 0 && oa % (W * sizeof(TO)) == 0;
+    P.total = m * (wide ? P.n / W : P.n);
+    const uint64_t blocks = (P.total + COMBINE_THREADS - 1) / COMBINE_THREADS;
+    const uint32_t grid = (uint32_t)tmin<uint64_t>(blocks, 1u << 20);
+    if (wide) combine_kernel<TZ, TO, W><<<grid, COMBINE_THREADS, 0, st>>>(P);
+    else combine_kernel<TZ, TO, 1><<<grid, COMBINE_THREADS, 0, st>>>(P);
+    return cudaGetLastError();
+}
+
+template <typename TZ>
+cudaError_t launch_z(const CombineParams &P, uint64_t m, int out_dtype, cudaStream_t st) {
+    if (out_dtype == DT_F32) return launch_t<TZ, float>(P, m, st);
+    if (out_dtype == DT_BF16) return launch_t<TZ, __nv_bfloat16>(P, m, st);
+    return launch_t<TZ, __half>(P, m, st);
+}
+
+}  // namespace
+
+cudaError_t launch_combine(const void *z, const float *weights, const uint32_t *ids, const void *residual, void *out,
+                           uint32_t m, uint32_t S, uint32_t n, uint32_t E, int z_dtype, int out_dtype,
+                           cudaStream_t st) {
+    const CombineParams P{z, weights, ids, residual, out, 0, S, n, E};
+    if (z_dtype == DT_F32) return launch_z<float>(P, m, out_dtype, st);
+    if (z_dtype == DT_BF16) return launch_z<__nv_bfloat16>(P, m, out_dtype, st);
+    return launch_z<__half>(P, m, out_dtype, st);
+}
+
+}  // namespace moe
+
+extern "C" moe_status moe_combine(const void *z, const float *weights, const uint32_t *ids, const void *residual,
+                                  void *out, uint32_t m, uint32_t n_expert_used, uint32_t n, uint32_t num_experts,
+                                  moe_dtype z_dtype, moe_dtype out_dtype, moe_stream_t stream) {
+    if (!m || !n_expert_used || !n || (ids && !num_experts)) return MOE_ERR_INVALID_ARGUMENT;
+    if ((int)z_dtype < 0 || (int)z_dtype > 2 || (int)out_dtype < 0 || (int)out_dtype > 2)
+        return MOE_ERR_INVALID_ARGUMENT;
+    if (!z || !weights || !out) return MOE_ERR_INVALID_ARGUMENT;
+    const uintptr_t zm = z_dtype == MOE_F32 ? 3u : 1u, om = out_dtype == MOE_F32 ? 3u : 1u;
+    if (((uintptr_t)z & zm) || (((uintptr_t)out | (uintptr_t)residual) & om) ||
+        (((uintptr_t)weights | (uintptr_t)ids) & 3u))
+        return MOE_ERR_INVALID_ARGUMENT;
+    if ((uint64_t)m * n_expert_used > 0x7FFFFFFFull) return MOE_ERR_UNSUPPORTED;
+    return moe::launch_combine(z, weights, ids, residual, out, m, n_expert_used, n, num_experts, (int)z_dtype,
+                               (int)out_dtype, (cudaStream_t)stream) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}

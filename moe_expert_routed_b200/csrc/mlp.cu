@@ -1,0 +1,108 @@
+// mlp.cu -- the gated expert MLP of a layer (include/moe_qmm.h, moe_mlp):
+//   h[t][s]  = act(G_e x_t) * (U_e x_t),        e = ids[t][s]
+//   out[t]   = residual[t] + sum_s weights[t][s] * (D_e h[t][s])
+// Two ways, chosen by size:
+//   few tokens   the two kernels of mlp_few.cu (the sum over the slots happens in
+//                the down projection's kernel);
+//   otherwise    the fused gate+up product, the down product over the pairs and the
+//                weighted sum, each a call of this library.
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+inline size_t al256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// Type of h between the two products. bf16 x: bf16, the rounding every bf16 model
+// makes there (it adds 2^-9 of each h once, next to the 2^-9 of the result's own
+// rounding, and has f32's range). f16 and f32 x: f32, since |h| can leave f16's
+// range (two factors) and bf16 would cost an f16 result 3 of its bits.
+moe_dtype h_dtype(int x_dtype) { return x_dtype == DT_BF16 ? MOE_BF16 : MOE_F32; }
+
+struct Layout {
+    size_t own, h, z, total;  // own: workspace of the products, at offset 0 (the error word first)
+};
+
+bool layout(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t S, uint32_t E, int x_dtype, Layout *L) {
+    const uint64_t R = (uint64_t)m * S;
+    if (R > 0x7FFFFFFFull) return false;
+    const moe_dtype hd = h_dtype(x_dtype);
+    const size_t a = moe_qmm_id_workspace_bytes_k(m, hidden, S, E, (moe_dtype)x_dtype);
+    const size_t b = moe_qmm_id_workspace_bytes_k((uint32_t)R, inter, 1, E, hd);
+    if (!a || !b) return false;
+    L->own = al256(a > b ? a : b);
+    L->h = L->own;
+    L->z = L->h + al256(R * inter * (hd == MOE_F32 ? 4ull : 2ull));
+    L->total = L->z + al256(R * hidden * 4ull);
+    return true;
+}
+
+moe_status check_weights(const moe_expert_weights *w, uint32_t k, uint32_t n) {
+    if (!w) return MOE_ERR_INVALID_ARGUMENT;
+    if (w->bias && ((int)w->bias_dtype < 0 || (int)w->bias_dtype > 2)) return MOE_ERR_INVALID_ARGUMENT;
+    // sizes, formats and pointers by the rules of the product itself
+    return validate_call(w->packed, (const uint32_t *)w->packed, w->packed, w->scales, w->aux, w->packed, 1, k, n,
+                         w->group_size, w->bits, w->fmt, 1, 1, MOE_F32, MOE_F32);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_mlp_workspace_bytes(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t n_expert_used,
+                               uint32_t num_experts, moe_dtype x_dtype) {
+    Layout L;
+    if (!m || !hidden || !inter || !n_expert_used || !num_experts || (int)x_dtype < 0 || (int)x_dtype > 2) return 0;
+    return layout(m, hidden, inter, n_expert_used, num_experts, (int)x_dtype, &L) ? L.total : 0;
+}
+
+moe_status moe_mlp(const void *x, const uint32_t *ids, const float *weights, const moe_expert_weights *gate_up,
+                   const moe_expert_weights *down, const void *residual, void *out, uint32_t m, uint32_t hidden,
+                   uint32_t inter, uint32_t n_expert_used, uint32_t num_experts, moe_dtype x_dtype,
+                   moe_dtype out_dtype, moe_act act, void *workspace, size_t workspace_bytes, moe_stream_t stream,
+                   moe_path path) {
+    if (!m || !hidden || !inter || !n_expert_used || !num_experts || inter > 0x7FFFFFFFu)
+        return MOE_ERR_INVALID_ARGUMENT;
+    if ((int)x_dtype < 0 || (int)x_dtype > 2 || (int)out_dtype < 0 || (int)out_dtype > 2 || (int)act < 0 ||
+        (int)act > 2 || (int)path < 0 || (int)path > 2)
+        return MOE_ERR_INVALID_ARGUMENT;
+    if (!x || !ids || !weights || !out) return MOE_ERR_INVALID_ARGUMENT;
+    moe_status v = check_weights(gate_up, hidden, 2u * inter);
+    if (v == MOE_OK) v = check_weights(down, inter, hidden);
+    if (v != MOE_OK) return v;
+    const uintptr_t xm = x_dtype == MOE_F32 ? 3u : 1u, om = out_dtype == MOE_F32 ? 3u : 1u;
+    if (((uintptr_t)x & xm) || (((uintptr_t)out | (uintptr_t)residual) & om) ||
+        (((uintptr_t)ids | (uintptr_t)weights) & 3u) || !workspace || ((uintptr_t)workspace & 15u))
+        return MOE_ERR_INVALID_ARGUMENT;
+    Layout L;
+    if (!layout(m, hidden, inter, n_expert_used, num_experts, (int)x_dtype, &L)) return MOE_ERR_UNSUPPORTED;
+    if (workspace_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+
+    uint8_t *ws = (uint8_t *)workspace;
+    const uint32_t R = m * n_expert_used;
+    void *h = ws + L.h, *z = ws + L.z;
+    const moe_dtype hd = h_dtype((int)x_dtype);
+    v = moe_qmm_id_glu(x, ids, gate_up->packed, gate_up->scales, gate_up->aux, gate_up->bias, h, m, hidden,
+                       2u * inter, gate_up->group_size, gate_up->bits, gate_up->fmt, n_expert_used, num_experts,
+                       x_dtype, hd, gate_up->bias_dtype, act, workspace, L.own, stream, path);
+    if (v != MOE_OK) return v;
+    // every (token, slot) pair is a token of its own here, with its own row of h
+    if (down->bias)
+        v = moe_qmm_id_bias(h, ids, down->packed, down->scales, down->aux, down->bias, z, R, inter, hidden,
+                            down->group_size, down->bits, down->fmt, 1, num_experts, hd, MOE_F32, down->bias_dtype,
+                            workspace, L.own, stream, path);
+    else
+        v = moe_qmm_id_path(h, ids, down->packed, down->scales, down->aux, z, R, inter, hidden, down->group_size,
+                            down->bits, down->fmt, 1, num_experts, hd, MOE_F32, workspace, L.own, stream, path);
+    if (v != MOE_OK) return v;
+    return launch_combine(z, weights, ids, residual, out, m, n_expert_used, hidden, num_experts, DT_F32,
+                          (int)out_dtype, (cudaStream_t)stream) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+}  // extern "C"
