@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libmoe_qmm.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["api.cu", "route.cu", "gemv.cu", "gemm_sm100.cu", "noalloc.cu", "actq.cu", "gemm_w4a4.cu",
-           "gate.cu", "combine.cu", "mlp.cu"]
+           "gate.cu", "combine.cu", "mlp.cu", "mlp_few.cu"]
 HEADERS = ["common.cuh", "ptx.cuh", "internal.h", "gemv_common.cuh"]
 
 NVCC_FLAGS = [

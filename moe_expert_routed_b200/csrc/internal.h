@@ -132,6 +132,22 @@ cudaError_t launch_combine(const void *z, const float *weights, const uint32_t *
                            uint32_t m, uint32_t S, uint32_t n, uint32_t E, int z_dtype, int out_dtype,
                            cudaStream_t st);
 
+// moe_mlp's checked arguments.
+struct MlpArgs {
+    const void *x;
+    const uint32_t *ids;
+    const float *weights;
+    const moe_expert_weights *gate_up, *down;
+    const void *residual;
+    void *out;
+    uint32_t m, hidden, inter, S, E;
+    int x_dtype, out_dtype, act;
+};
+// The two kernels for few tokens: what they take, the bytes of h's planes, the launch.
+bool mlp_few_supported(const MlpArgs &a);
+uint64_t mlp_few_workspace(uint32_t m, uint32_t inter, uint32_t S);
+cudaError_t launch_mlp_few(const MlpArgs &a, uint32_t *err, void *hf, cudaStream_t st);
+
 // moe_qmm_id's scalar validation (MOE_OK or the status moe_qmm_id would return).
 moe_status validate_call(const void *x, const uint32_t *ids, const void *packed, const void *scales,
                          const void *aux, const void *out, uint32_t m, uint32_t k, uint32_t n,

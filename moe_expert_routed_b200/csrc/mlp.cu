@@ -28,6 +28,7 @@ bool layout(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t S, uint32_t E,
     const uint64_t R = (uint64_t)m * S;
     if (R > 0x7FFFFFFFull) return false;
     const moe_dtype hd = h_dtype(x_dtype);
+    const uint64_t few = mlp_few_workspace(m, inter, S);
     const size_t a = moe_qmm_id_workspace_bytes_k(m, hidden, S, E, (moe_dtype)x_dtype);
     const size_t b = moe_qmm_id_workspace_bytes_k((uint32_t)R, inter, 1, E, hd);
     if (!a || !b) return false;
@@ -35,6 +36,8 @@ bool layout(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t S, uint32_t E,
     L->h = L->own;
     L->z = L->h + al256(R * inter * (hd == MOE_F32 ? 4ull : 2ull));
     L->total = L->z + al256(R * hidden * 4ull);
+    // the few-token kernels' planes of h take the same room
+    if (L->total < L->h + al256(few)) L->total = L->h + al256(few);
     return true;
 }
 
@@ -85,6 +88,10 @@ moe_status moe_mlp(const void *x, const uint32_t *ids, const float *weights, con
     uint8_t *ws = (uint8_t *)workspace;
     const uint32_t R = m * n_expert_used;
     void *h = ws + L.h, *z = ws + L.z;
+    const MlpArgs a{x,      ids,   weights, gate_up,       down,        residual,     out,           m,
+                    hidden, inter, n_expert_used, num_experts, (int)x_dtype, (int)out_dtype, (int)act};
+    if (path != MOE_PATH_GROUPED && mlp_few_supported(a))
+        return launch_mlp_few(a, (uint32_t *)ws, h, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     const moe_dtype hd = h_dtype((int)x_dtype);
     v = moe_qmm_id_glu(x, ids, gate_up->packed, gate_up->scales, gate_up->aux, gate_up->bias, h, m, hidden,
                        2u * inter, gate_up->group_size, gate_up->bits, gate_up->fmt, n_expert_used, num_experts,
