@@ -41,8 +41,11 @@ constexpr uint32_t FULL = 0xFFFFFFFFu;
 constexpr uint32_t FEW_THREADS = 256, FEW_WARPS = 8;
 constexpr uint32_t FEW_MAX_R = 256;      // pairs (one thread each in the prologues)
 constexpr uint32_t FEW_MAX_TOKENS = 64;  // rows of mlp_down's per-warp sums
-constexpr uint32_t UP_TILES = 4;         // tiles of a CTA's 64 rows
-constexpr size_t FEW_SMEM_TWO = 110 * 1024, FEW_SMEM_ONE = 220 * 1024;  // two CTAs or one an SM
+constexpr uint32_t TILES = 2;            // tiles of 16 rows a warp works on at once
+constexpr uint32_t UP_PARTS = 4;         // mlp_up: warps that share a pair of tiles, each a part of hidden
+constexpr uint32_t RING = 4;             // steps of a warp in flight
+constexpr size_t UP_RING = FEW_WARPS * RING * TILES * 1024;
+constexpr size_t FEW_SMEM = 220 * 1024;
 
 // Planes of x by its type, of h by the result's.
 constexpr int x_planes(int dt) { return dt == DT_F32 ? 2 : 1; }
@@ -125,70 +128,79 @@ struct StepB {
     float f[NB][2], xs[NB][2];
 };
 
-// From the pairs' step images at `base`; pairs at and past np are 0.
+// From the pairs' step images at `base`, `stride` bytes apart; pairs at and past np are
+// 0, as are the lanes whose k are not their column's unit: they read `zeros` (64 bytes).
 template <int KIND, int PLANES, int NB>
-__device__ __forceinline__ void load_step(StepB<NB> &S, const uint8_t *base, uint32_t np, uint32_t lane) {
-    constexpr uint32_t STRIDE = step_bytes(PLANES);
+__device__ __forceinline__ void load_step(StepB<NB> &S, const uint8_t *base, uint32_t stride, const uint8_t *zeros,
+                                          uint32_t np, uint32_t lane) {
     const uint32_t q = lane & 3u;
     const bool active = ((lane >> 2) & 3u) == q;  // this lane's k of column lane / 4 are that column's unit
 #pragma unroll
     for (uint32_t n = 0; n < NB; n++) {
         const uint32_t set = 2u * n + (lane >> 4), pair = set / PLANES, plane = set % PLANES;
         uint32_t(&b)[16] = S.b[n];
-        if (active && pair < np) {
-            const uint4 *v = (const uint4 *)(base + pair * STRIDE + plane * 256u + q * 64u);
+        const uint4 *v = (const uint4 *)(active && pair < np ? base + pair * stride + plane * 256u + q * 64u : zeros);
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const uint4 x = v[i];
-                b[4 * i] = x.x; b[4 * i + 1] = x.y; b[4 * i + 2] = x.z; b[4 * i + 3] = x.w;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; i++) b[i] = 0u;
+        for (int i = 0; i < 4; i++) {
+            const uint4 x = v[i];
+            b[4 * i] = x.x; b[4 * i + 1] = x.y; b[4 * i + 2] = x.z; b[4 * i + 3] = x.w;
         }
         // the lane's accumulator columns 2q, 2q + 1: units 2 (q mod 2) and the next of set 2n + q / 2
         const uint32_t cset = 2u * n + (q >> 1), cpair = cset / PLANES, cplane = cset % PLANES;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (cpair < np) v = *(const float4 *)(base + cpair * STRIDE + PLANES * 256u + (q & 1u) * 16u);
+        const float4 f = *(const float4 *)(cpair < np ? base + cpair * stride + PLANES * 256u + (q & 1u) * 16u : zeros);
         const float unit = cplane ? code_unit<KIND> * 4.8828125e-4f : code_unit<KIND>;  // 2^-11
-        S.f[n][0] = v.x * unit;
-        S.f[n][1] = v.z * unit;
-        S.xs[n][0] = cplane ? 0.f : v.y;  // the bias once a pair
-        S.xs[n][1] = cplane ? 0.f : v.w;
+        S.f[n][0] = f.x * unit;
+        S.f[n][1] = f.z * unit;
+        S.xs[n][0] = cplane ? 0.f : f.y;  // the bias once a pair
+        S.xs[n][1] = cplane ? 0.f : f.w;
     }
 }
 
-// 16 rows x 4 units: wa, wb the lane's unit of rows r and r + 8; sa, sb those rows' scales,
-// ba, bb their biases; u0, u1 the units of the lane's accumulator columns.
-template <int KIND, int NB>
-__device__ __forceinline__ void tile_step(const uint4 wa, const uint4 wb, const StepB<NB> &S, const uint8_t *sa,
-                                          const uint8_t *sb, const uint8_t *ba, const uint8_t *bb, uint32_t u0,
-                                          uint32_t u1, uint32_t gshift, float (&acc)[NB][2]) {
-    const uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w}, b[4] = {wb.x, wb.y, wb.z, wb.w};
-    constexpr int PARTS = KIND == K_NVFP4 ? 2 : 1;  // scale groups in a unit
-    float s[PARTS][4];                              // of (row r, u0), (r, u1), (r + 8, u0), (r + 8, u1)
+// Scales (and affine biases) that a lane applies: of rows r and r + 8 and the two units of
+// its accumulator columns; NVFP4 units have two.
+template <int KIND>
+struct Scales {
+    static constexpr int PARTS = KIND == K_NVFP4 ? 2 : 1;
+    float s[PARTS][4];  // (row r, unit 0), (r, 1), (r + 8, 0), (r + 8, 1)
+    float b[4];
+};
+
+// From the two rows' scales and biases, at the units' entries i0, i1 (affine: of their
+// groups; one group for both where `same`).
+template <int KIND>
+__device__ __forceinline__ void load_scales(Scales<KIND> &S, const uint8_t *sa, const uint8_t *sb, const uint8_t *ba,
+                                            const uint8_t *bb, uint32_t i0, uint32_t i1, bool same) {
     if constexpr (KIND == K_AFF4) {
-        const uint32_t g0 = u0 >> gshift, g1 = u1 >> gshift;
-        s[0][0] = bf16_bits_to_f32(((const unsigned short *)sa)[g0]);
-        s[0][2] = bf16_bits_to_f32(((const unsigned short *)sb)[g0]);
-        s[0][1] = s[0][0];
-        s[0][3] = s[0][2];
-        if (gshift == 0u) {  // groups of one unit
-            s[0][1] = bf16_bits_to_f32(((const unsigned short *)sa)[g1]);
-            s[0][3] = bf16_bits_to_f32(((const unsigned short *)sb)[g1]);
+        S.s[0][0] = S.s[0][1] = bf16_bits_to_f32(((const unsigned short *)sa)[i0]);
+        S.s[0][2] = S.s[0][3] = bf16_bits_to_f32(((const unsigned short *)sb)[i0]);
+        S.b[0] = S.b[1] = bf16_bits_to_f32(((const unsigned short *)ba)[i0]);
+        S.b[2] = S.b[3] = bf16_bits_to_f32(((const unsigned short *)bb)[i0]);
+        if (!same) {
+            S.s[0][1] = bf16_bits_to_f32(((const unsigned short *)sa)[i1]);
+            S.s[0][3] = bf16_bits_to_f32(((const unsigned short *)sb)[i1]);
+            S.b[1] = bf16_bits_to_f32(((const unsigned short *)ba)[i1]);
+            S.b[3] = bf16_bits_to_f32(((const unsigned short *)bb)[i1]);
         }
     } else if constexpr (KIND == K_MXFP4) {
-        s[0][0] = e8m0_to_f32(sa[u0]);
-        s[0][1] = e8m0_to_f32(sa[u1]);
-        s[0][2] = e8m0_to_f32(sb[u0]);
-        s[0][3] = e8m0_to_f32(sb[u1]);
+        S.s[0][0] = e8m0_to_f32(sa[i0]);
+        S.s[0][1] = e8m0_to_f32(sa[i1]);
+        S.s[0][2] = e8m0_to_f32(sb[i0]);
+        S.s[0][3] = e8m0_to_f32(sb[i1]);
     } else {
-        from_e4m3x2(((const unsigned short *)sa)[u0], s[0][0], s[PARTS - 1][0]);
-        from_e4m3x2(((const unsigned short *)sa)[u1], s[0][1], s[PARTS - 1][1]);
-        from_e4m3x2(((const unsigned short *)sb)[u0], s[0][2], s[PARTS - 1][2]);
-        from_e4m3x2(((const unsigned short *)sb)[u1], s[0][3], s[PARTS - 1][3]);
+        constexpr int L = Scales<KIND>::PARTS - 1;
+        from_e4m3x2(((const unsigned short *)sa)[i0], S.s[0][0], S.s[L][0]);
+        from_e4m3x2(((const unsigned short *)sa)[i1], S.s[0][1], S.s[L][1]);
+        from_e4m3x2(((const unsigned short *)sb)[i0], S.s[0][2], S.s[L][2]);
+        from_e4m3x2(((const unsigned short *)sb)[i1], S.s[0][3], S.s[L][3]);
     }
-    constexpr int WPP = 4 / PARTS;  // words a part
+}
+
+// 16 rows x 4 units: wa, wb the lane's unit of rows r and r + 8.
+template <int KIND, int NB>
+__device__ __forceinline__ void tile_step(const uint4 wa, const uint4 wb, const StepB<NB> &S, const Scales<KIND> &C,
+                                          float (&acc)[NB][2]) {
+    const uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w}, b[4] = {wb.x, wb.y, wb.z, wb.w};
+    constexpr int PARTS = Scales<KIND>::PARTS, WPP = 4 / PARTS;  // words a part
 #pragma unroll
     for (int h = 0; h < PARTS; h++) {
         float c[NB][4];
@@ -208,22 +220,15 @@ __device__ __forceinline__ void tile_step(const uint4 wa, const uint4 wb, const 
         }
 #pragma unroll
         for (int n = 0; n < NB; n++) {
-            acc[n][0] = fmaf(s[h][0], c[n][0] * S.f[n][0], fmaf(s[h][1], c[n][1] * S.f[n][1], acc[n][0]));
-            acc[n][1] = fmaf(s[h][2], c[n][2] * S.f[n][0], fmaf(s[h][3], c[n][3] * S.f[n][1], acc[n][1]));
+            acc[n][0] = fmaf(C.s[h][0], c[n][0] * S.f[n][0], fmaf(C.s[h][1], c[n][1] * S.f[n][1], acc[n][0]));
+            acc[n][1] = fmaf(C.s[h][2], c[n][2] * S.f[n][0], fmaf(C.s[h][3], c[n][3] * S.f[n][1], acc[n][1]));
         }
     }
     if constexpr (affine_kind<KIND>) {
-        const uint32_t g0 = u0 >> gshift, g1 = u1 >> gshift;
-        float b0 = bf16_bits_to_f32(((const unsigned short *)ba)[g0]), b1 = b0;
-        float b2 = bf16_bits_to_f32(((const unsigned short *)bb)[g0]), b3 = b2;
-        if (gshift == 0u) {
-            b1 = bf16_bits_to_f32(((const unsigned short *)ba)[g1]);
-            b3 = bf16_bits_to_f32(((const unsigned short *)bb)[g1]);
-        }
 #pragma unroll
         for (int n = 0; n < NB; n++) {
-            acc[n][0] = fmaf(b0, S.xs[n][0], fmaf(b1, S.xs[n][1], acc[n][0]));
-            acc[n][1] = fmaf(b2, S.xs[n][0], fmaf(b3, S.xs[n][1], acc[n][1]));
+            acc[n][0] = fmaf(C.b[0], S.xs[n][0], fmaf(C.b[1], S.xs[n][1], acc[n][0]));
+            acc[n][1] = fmaf(C.b[2], S.xs[n][0], fmaf(C.b[3], S.xs[n][1], acc[n][1]));
         }
     }
 }
@@ -252,17 +257,28 @@ __device__ __forceinline__ uint32_t expert_mask(uint32_t id, bool valid, uint32_
     return base[32];
 }
 
-// cp.async groups that may still be in flight.
-__device__ __forceinline__ void wait_groups(uint32_t n) {
-    switch (n) {
-        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-        case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-        case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-        case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-        case 7: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
-        default: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    }
+template <int N>
+__device__ __forceinline__ void wait_groups() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Thread block clusters: this block's rank, the barrier, and a load from the shared
+// memory of the block of another rank at this block's address.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float cluster_load(uint32_t addr, uint32_t rank) {
+    float v;
+    asm volatile("{.reg .u32 a; mapa.shared::cluster.u32 a, %1, %2; ld.shared::cluster.f32 %0, [a];}"
+                 : "=f"(v)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return v;
 }
 
 // --------------------------------------------------------------- projections
@@ -283,7 +299,7 @@ struct FewParams {
     uint32_t g1, g2, gshift1, gshift2;  // groups of a row; log2(units of 32 a group)
     int x_dtype, out_dtype, bias1_dtype, bias2_dtype, act;
     int scale2_kind, down_affine;    // 1: the down projection is NVFP4 (scale2 in a2); affine
-    uint32_t stages, slots, max_parts;  // ring depth; mlp_down: experts whose scales it holds, parts an expert
+    uint32_t cluster;                // mlp_down: blocks that share 32 columns
 };
 
 // Four consecutive x values.
@@ -345,69 +361,99 @@ __device__ __forceinline__ void write_step(uint8_t *dst, float4 v, uint32_t lane
 // mlp_up. grid (inter / 32, ranks of distinct experts). A CTA holds 32 columns of h, a
 // unit of mlp_down (64 weight rows: tile t pairs gate rows 8t..8t+7 with up rows
 // 8t..8t+7, so that a lane's two accumulator rows are the gate and the up of one
-// column); its warps split hidden in steps of 128 codes.
+// column). Each pair of tiles has four warps, which take the steps of 128 codes in
+// turn; x is written as step images once for all of them. Two tiles a warp share a
+// step's B registers and its loop.
 template <int KIND, int XT, int NB>
 __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const FewParams P) {
     constexpr int PLANES = x_planes(XT), PP = 2 * NB / PLANES;  // pairs a pass
-    constexpr uint32_t STAGE = UP_TILES * 2 * 512, XSTEP = step_bytes(PLANES);
+    constexpr uint32_t STAGE = TILES * 2 * 512, XSTEP = step_bytes(PLANES);
     extern __shared__ __align__(16) uint8_t sm[];
+    __shared__ __align__(16) uint8_t zeros[64];
     __shared__ uint32_t mask[32], base[33], wcount[FEW_WARPS], pairs[FEW_MAX_R], expert_s;
 
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
+    if (tid < 16) ((uint32_t *)zeros)[tid] = 0u;
     // mlp_down may start from here on: what came before this kernel is complete
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
 
     // the expert of this rank and its pairs, ascending
-    const uint32_t id = tid < P.R ? __ldg(P.ids + tid) : FULL;
-    const bool valid = id < P.E;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && tid < P.R && !valid) atomicOr(P.err, ERR_BAD_ID);
-    if (blockIdx.y >= expert_mask(id, valid, mask, base)) return;
-    if (tid < 32 && base[tid] <= blockIdx.y && blockIdx.y < base[tid + 1]) {
-        uint32_t m = mask[tid];
-        for (uint32_t i = base[tid]; i < blockIdx.y; i++) m &= m - 1u;
-        expert_s = tid * 32u + __ffs(m) - 1u;
+    uint32_t e, np;
+    if (P.R <= 32u) {  // each warp by itself; ranks in the order of the experts' first pairs
+        const uint32_t id = lane < P.R ? __ldg(P.ids + lane) : FULL;
+        const bool valid = id < P.E;
+        if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0 && lane < P.R && !valid) atomicOr(P.err, ERR_BAD_ID);
+        const uint32_t same = __match_any_sync(FULL, id);
+        uint32_t firsts = __ballot_sync(FULL, valid && __ffs(same) - 1u == lane);
+        if (blockIdx.y >= __popc(firsts)) return;
+        for (uint32_t i = 0; i < blockIdx.y; i++) firsts &= firsts - 1u;
+        e = __shfl_sync(FULL, id, __ffs(firsts) - 1);
+        const uint32_t mine = __ballot_sync(FULL, valid && id == e);
+        np = __popc(mine);
+        if (warp == 0 && valid && id == e) pairs[__popc(mine & ((1u << lane) - 1u))] = lane;
+    } else {
+        const uint32_t id = tid < P.R ? __ldg(P.ids + tid) : FULL;
+        const bool valid = id < P.E;
+        if (blockIdx.x == 0 && blockIdx.y == 0 && tid < P.R && !valid) atomicOr(P.err, ERR_BAD_ID);
+        if (blockIdx.y >= expert_mask(id, valid, mask, base)) return;
+        if (tid < 32 && base[tid] <= blockIdx.y && blockIdx.y < base[tid + 1]) {
+            uint32_t m = mask[tid];
+            for (uint32_t i = base[tid]; i < blockIdx.y; i++) m &= m - 1u;
+            expert_s = tid * 32u + __ffs(m) - 1u;
+        }
+        __syncthreads();
+        e = expert_s;
+        const uint32_t mine = __ballot_sync(FULL, valid && id == e);
+        if (lane == 0) wcount[warp] = __popc(mine);
+        __syncthreads();
+        uint32_t at = 0;
+        np = 0;
+#pragma unroll
+        for (uint32_t i = 0; i < FEW_WARPS; i++) {
+            if (i < warp) at += wcount[i];
+            np += wcount[i];
+        }
+        if (valid && id == e) pairs[at + __popc(mine & ((1u << lane) - 1u))] = tid;
     }
-    __syncthreads();
-    const uint32_t e = expert_s;
 
-    const uint32_t r = lane >> 2, q = lane & 3u;
+    const uint32_t r = lane >> 2, q = lane & 3u, tp = warp & 1u, part = warp >> 1;
     const uint32_t nu = P.H / 32u, steps = (nu + 3u) / 4u;
     const uint32_t row_bytes = P.H / 2u;
     const uint32_t c0 = blockIdx.x * 32u;
     const uint32_t srow = scale_bytes(KIND, P.g1);
-    uint8_t *const xb = sm + FEW_WARPS * P.stages * STAGE + warp * PP * XSTEP;  // this warp's step images
-    uint8_t *const s_s = sm + FEW_WARPS * (P.stages * STAGE + PP * XSTEP);
+    uint8_t *const images = sm + FEW_WARPS * RING * STAGE;  // [pair][step]
+    uint8_t *const s_s = images + PP * steps * XSTEP;
     uint8_t *const b_s = s_s + 64u * srow;
     const uint32_t sm0 = ptx::smem_u32(sm);
-    const uint32_t ring = sm0 + warp * P.stages * STAGE + lane * 16u;
-    const uint8_t *const wrow = P.w1 + ((size_t)e * 2u * P.I + c0 + r) * row_bytes + q * 16u;  // gate row of tile 0
-    const size_t up = (size_t)P.I * row_bytes, trow = 8u * (size_t)row_bytes;
-    const uint32_t n_mine = warp < steps ? (steps - warp + FEW_WARPS - 1u) / FEW_WARPS : 0u;
+    const uint32_t ring = sm0 + warp * RING * STAGE + lane * 16u;
+    // this lane's unit of its rows of the first tile
+    const uint8_t *const wrow = P.w1 + ((size_t)e * 2u * P.I + c0 + 16u * tp + r) * row_bytes + q * 16u;
+    const size_t up = (size_t)P.I * row_bytes, next = 8u * (size_t)row_bytes;
 
-    // the weights of a step into the ring: this lane's unit of each of the 8 row groups
     const uint8_t *src = wrow;
-    uint32_t ju = 0, is = 0;  // next step of this warp to request, its slot
+    uint32_t ju = 0, is = 0;  // next step to request, its slot
     auto issue = [&]() {
-        if (ju < n_mine) {
-            const uint32_t u = (warp + ju * FEW_WARPS) * 4u + q, size = u < nu ? 16u : 0u;
-            const uint8_t *g = size ? src : wrow;  // past the row: nothing is read, zeros are stored
-            const uint32_t st = ring + is * STAGE;
-#pragma unroll
-            for (uint32_t t = 0; t < UP_TILES; t++, g += trow) {
-                ptx::cp_async_16(st + (2 * t) * 512u, g, size);
-                ptx::cp_async_16(st + (2 * t + 1) * 512u, g + up, size);
-            }
-            src += FEW_WARPS * 64u;
-            is = is + 1u == P.stages ? 0u : is + 1u;
+        if (ju < steps) {
+            const uint32_t size = 4u * ju + q < nu ? 16u : 0u;  // past the row nothing is read, zeros are stored
+            const uint8_t *g = size ? src : wrow;
+            ptx::cp_async_16(ring + is, g, size);
+            ptx::cp_async_16(ring + is + 512u, g + up, size);
+            g += next;
+            ptx::cp_async_16(ring + is + 1024u, g, size);
+            ptx::cp_async_16(ring + is + 1536u, g + up, size);
+            src += UP_PARTS * 64u;
+            is = (is + STAGE) & (RING * STAGE - 1u);
+            ju += UP_PARTS;
         }
-        ju++;
         ptx::cp_async_commit();
     };
     auto restart = [&]() {
-        src = wrow + warp * 64u;
-        ju = is = 0u;
-        for (uint32_t i = 0; i < P.stages; i++) issue();
+        src = wrow + part * 64u;
+        ju = part;
+        is = 0u;
+#pragma unroll
+        for (uint32_t i = 0; i < RING; i++) issue();
     };
 
     // scales (and affine biases) of the 64 rows: two blocks of 32 contiguous rows each
@@ -419,70 +465,69 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const Few
     }
     ptx::cp_async_commit();
     restart();
-
-    const uint32_t mine = __ballot_sync(FULL, valid && id == e);
-    if (lane == 0) wcount[warp] = __popc(mine);
-    __syncthreads();
-    uint32_t np = 0, at = 0;
-#pragma unroll
-    for (uint32_t i = 0; i < FEW_WARPS; i++) {
-        if (i < warp) at += wcount[i];
-        np += wcount[i];
-    }
-    if (valid && id == e) pairs[at + __popc(mine & ((1u << lane) - 1u))] = tid;
-    wait_groups(P.stages);  // the scales' group is the oldest
-    __syncthreads();        // pairs[], and the other threads' parts of the scales
+    __syncthreads();  // pairs[]
 
     for (uint32_t pb = 0; pb < np; pb += PP) {
         const uint32_t npass = tmin<uint32_t>(PP, np - pb);
         if (pb) restart();
-        size_t xrow[PP];
-        float4 xv[PP];
-        auto fetch_x = [&](uint32_t i) {  // the lane's 4 values of each pair's step
-            const uint32_t k = (warp + i * FEW_WARPS) * 128u + 4u * lane;
+        for (uint32_t p = 0; p < npass; p++) {
+            const size_t xrow = (size_t)(pairs[pb + p] / P.S) * P.H + 4u * lane;
+#pragma unroll 4
+            for (uint32_t j = warp; j < steps; j += FEW_WARPS) {
+                const float4 v = j * 128u + 4u * lane < P.H ? load_x4<XT>(P.x, xrow + j * 128u)
+                                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                write_step<KIND, PLANES>(images + (p * steps + j) * XSTEP, v, lane);
+            }
+        }
+        // what the epilogue of this warp's pair needs, requested now (a pass has at most 8)
+        const bool mine = warp < npass;
+        const uint32_t p_e = mine ? pairs[pb + warp] : 0u, c = c0 + lane;
+        float weight = 0.f, bg = 0.f, bu = 0.f;
+        if (mine) {
+            weight = __ldg(P.weights + p_e);
+            if (P.scale2_kind) weight *= __ldg((const float *)P.a2 + e);
+            bg = load_bias(P.bias1, P.bias1_dtype, (size_t)e * 2u * P.I + c);
+            bu = load_bias(P.bias1, P.bias1_dtype, (size_t)e * 2u * P.I + P.I + c);
+        }
+        if (pb == 0) wait_groups<RING>();  // the scales' group is the oldest
+        __syncthreads();                   // images, and the other threads' parts of the scales
+
+        float acc[TILES][NB][2];
 #pragma unroll
-            for (uint32_t p = 0; p < PP; p++)
-                xv[p] = p < npass && i < n_mine && k < P.H ? load_x4<XT>(P.x, xrow[p] + k)
-                                                           : make_float4(0.f, 0.f, 0.f, 0.f);
-        };
-#pragma unroll
-        for (uint32_t p = 0; p < PP; p++) xrow[p] = p < npass ? (size_t)(pairs[pb + p] / P.S) * P.H : 0u;
-        fetch_x(0);
-        float acc[UP_TILES][NB][2];
-#pragma unroll
-        for (uint32_t t = 0; t < UP_TILES; t++)
+        for (uint32_t t = 0; t < TILES; t++)
 #pragma unroll
             for (int n = 0; n < NB; n++) acc[t][n][0] = acc[t][n][1] = 0.f;
-
-        const uint8_t *st = sm + warp * P.stages * STAGE + lane * 16u;
+        const uint8_t *st = sm + warp * RING * STAGE + lane * 16u;
+        const uint8_t *const sr = s_s + (16u * tp + r) * srow, *const br = b_s + (16u * tp + r) * srow;
+        const uint8_t *img = images + part * XSTEP;
         uint32_t slot = 0;
-        for (uint32_t i = 0; i < n_mine; i++) {
-#pragma unroll
-            for (uint32_t p = 0; p < PP; p++)
-                if (p < npass) write_step<KIND, PLANES>(xb + p * XSTEP, xv[p], lane);
-            __syncwarp();
+        for (uint32_t j = part; j < steps; j += UP_PARTS) {
             StepB<NB> B;
-            load_step<KIND, PLANES, NB>(B, xb, npass, lane);
-            __syncwarp();  // read before the next step's image is written
-            fetch_x(i + 1u);
-            wait_groups(P.stages - 1u);
-            const uint32_t u = 4u * (warp + i * FEW_WARPS) + 2u * (q & 1u);
-            const uint32_t u0 = tmin<uint32_t>(u, nu - 1u), u1 = tmin<uint32_t>(u + 1u, nu - 1u);
-            const uint8_t *w = st + slot * STAGE;
-            uint32_t so = r * srow;
+            load_step<KIND, PLANES, NB>(B, img, steps * XSTEP, zeros, npass, lane);
+            img += UP_PARTS * XSTEP;
+            const uint32_t u = 4u * j + 2u * (q & 1u);
+            uint32_t i0 = tmin<uint32_t>(u, nu - 1u), i1 = tmin<uint32_t>(u + 1u, nu - 1u);
+            if constexpr (affine_kind<KIND>) {
+                i0 >>= P.gshift1;
+                i1 >>= P.gshift1;
+            }
+            wait_groups<RING - 1>();
 #pragma unroll
-            for (uint32_t t = 0; t < UP_TILES; t++, so += 8u * srow)
-                tile_step<KIND, NB>(*(const uint4 *)(w + 2 * t * 512), *(const uint4 *)(w + (2 * t + 1) * 512), B,
-                                    s_s + so, s_s + so + 32u * srow, b_s + so, b_s + so + 32u * srow, u0, u1,
-                                    P.gshift1, acc[t]);
-            slot = slot + 1u == P.stages ? 0u : slot + 1u;
+            for (uint32_t t = 0; t < TILES; t++) {
+                const uint4 wa = *(const uint4 *)(st + slot + t * 1024u), wb = *(const uint4 *)(st + slot + t * 1024u + 512u);
+                Scales<KIND> C;
+                const uint32_t o = t * 8u * srow, ou = o + 32u * srow;
+                load_scales<KIND>(C, sr + o, sr + ou, br + o, br + ou, i0, i1, P.gshift1 != 0u);
+                tile_step<KIND, NB>(wa, wb, B, C, acc[t]);
+            }
+            slot = (slot + STAGE) & (RING * STAGE - 1u);
             issue();
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();  // the ring is free: the warps' sums go there
-        float *const red = (float *)sm;  // [warp][pair][gate / up][32 columns]
+        float *const red = (float *)sm;  // [part][pair][gate / up][32 columns]
 #pragma unroll
-        for (uint32_t t = 0; t < UP_TILES; t++)
+        for (uint32_t t = 0; t < TILES; t++)
 #pragma unroll
             for (int n = 0; n < NB; n++)
 #pragma unroll
@@ -492,76 +537,74 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const Few
                     if constexpr (PLANES == 2) v += __shfl_xor_sync(FULL, v, 2);
                     if (PLANES == 2 ? q == 0u : !(q & 1u)) {
                         const uint32_t p = PLANES == 2 ? n : 2u * n + (q >> 1);
-                        red[((warp * PP + p) * 2u + h) * 32u + 8u * t + r] = v;
+                        red[((part * PP + p) * 2u + h) * 32u + 16u * tp + 8u * t + r] = v;
                     }
                 }
         __syncthreads();
-        // one warp a pair: lane = column of h
-        for (uint32_t pi = warp; pi < npass; pi += FEW_WARPS) {
+        if (mine) {  // one warp a pair: lane = column of h
             float g = 0.f, v = 0.f;
 #pragma unroll
-            for (uint32_t w = 0; w < FEW_WARPS; w++) {
-                g += red[((w * PP + pi) * 2u) * 32u + lane];
-                v += red[((w * PP + pi) * 2u + 1u) * 32u + lane];
+            for (uint32_t k = 0; k < UP_PARTS; k++) {
+                g += red[((k * PP + warp) * 2u) * 32u + lane];
+                v += red[((k * PP + warp) * 2u + 1u) * 32u + lane];
             }
-            const uint32_t p = pairs[pb + pi], c = c0 + lane;
             if constexpr (KIND == K_NVFP4) {
                 const float s2 = __ldg((const float *)P.a1 + e);
                 g *= s2;
                 v *= s2;
             }
-            const size_t bo = (size_t)e * 2u * P.I + c;
-            g += load_bias(P.bias1, P.bias1_dtype, bo);
-            v += load_bias(P.bias1, P.bias1_dtype, bo + P.I);
-            float h = glu_act(P.act, g) * v * __ldg(P.weights + p);
-            if (P.scale2_kind) h *= __ldg((const float *)P.a2 + e);
+            float h = glu_act(P.act, g + bg) * (v + bu) * weight;
             // this unit of the pair's step image
             const int planes = h_planes(P.out_dtype);
             const uint32_t iu = P.I / 32u, un = blockIdx.x & 3u;
-            uint8_t *img = P.hf + ((size_t)p * ((iu + 3u) / 4u) + (blockIdx.x >> 2)) * step_bytes(planes);
-            const float sum = [&] {
-                float s = h;
+            uint8_t *img_h = P.hf + ((size_t)p_e * ((iu + 3u) / 4u) + (blockIdx.x >> 2)) * step_bytes(planes);
+            float sum = h;
 #pragma unroll
-                for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(FULL, s, d);
-                return s;
-            }();
+            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(FULL, sum, d);
             float scale, factor;
             unit_scale(__reduce_max_sync(FULL, __float_as_uint(h) & 0x7FFFFFFFu), scale, factor);
             h *= scale;
             if (b_sixteenth(P.down_affine, lane)) h *= 0.0625f;
-            uint16_t *dst = (uint16_t *)(img + un * 64u) + b_place(P.down_affine, lane);
+            uint16_t *dst = (uint16_t *)(img_h + un * 64u) + b_place(P.down_affine, lane);
             for (int k = 0; k < planes; k++, dst += 128) {
                 const __half b = __float2half_rn(h);
                 *dst = __half_as_ushort(b);
                 h = (h - __half2float(b)) * 2048.f;
             }
-            float2 *fs = (float2 *)(img + planes * 256);
+            float2 *fs = (float2 *)(img_h + planes * 256);
             if (lane == 0) fs[un] = make_float2(factor, sum);
             // units past inter in the last step are zero
             if (blockIdx.x + 1u == iu)
                 for (uint32_t z = un + 1u; z < 4u; z++) {
-                    for (int k = 0; k < planes; k++) ((uint16_t *)(img + k * 256 + z * 64u))[lane] = 0;
+                    for (int k = 0; k < planes; k++) ((uint16_t *)(img_h + k * 256 + z * 64u))[lane] = 0;
                     if (lane == 0) fs[z] = make_float2(0.f, 0.f);
                 }
         }
-        __syncthreads();  // red is read before the next pass's copies land there
+        if (pb + PP < np) __syncthreads();  // red is read before the next pass's copies land there
     }
 }
 
-// mlp_down. grid (hidden / 16): a CTA holds 16 columns of out. Its warps share the
-// distinct experts (an expert's rows in strided parts where there are few), each keeps
-// sums of its own for every token, added in warp order at the end: no atomics, one
-// order. Weights and scales do not depend on mlp_up, so the ring's first stages are
-// requested before waiting for it.
+// Scales of one step and row in mlp_down's ring: whole aligned words around the bytes.
+constexpr uint32_t DN_SROW = 12;
+
+// mlp_down. grid (hidden / 32 * cluster), a cluster of blocks for 32 columns of out (two
+// tiles a warp). The cluster's warps share the work items, (expert, part of its steps);
+// each keeps sums of its own for every token, added in warp order within a block and in
+// rank order through distributed shared memory: no atomics, one order. Weights and
+// scales do not depend on mlp_up, so the ring's first steps are requested before
+// waiting for it.
 template <int KIND, int NPL, int NB>
-__global__ void __launch_bounds__(FEW_THREADS, 2) mlp_down(const FewParams P) {
+__global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const FewParams P) {
     constexpr uint32_t PP = 2 * NB / NPL;  // pairs a pass
-    constexpr uint32_t HSTEP = step_bytes(NPL), WBYTES = 2 * 512, STAGE = WBYTES + PP * HSTEP;
+    constexpr uint32_t HSTEP = step_bytes(NPL), WBYTES = TILES * 2 * 512, SBYTES = 32 * DN_SROW;
+    constexpr uint32_t STAGE = WBYTES + PP * HSTEP + SBYTES * (affine_kind<KIND> ? 2 : 1);
     extern __shared__ __align__(16) uint8_t sm[];
+    __shared__ __align__(16) uint8_t zeros[64];
     __shared__ uint32_t mask[32], base[33], ids_s[FEW_MAX_R], first[FEW_MAX_R + 1], pairs[FEW_MAX_R],
         experts[FEW_MAX_R];
 
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
+    if (tid < 16) ((uint32_t *)zeros)[tid] = 0u;
     const uint32_t id = tid < P.R ? __ldg(P.ids + tid) : FULL;  // complete before mlp_up began
     const bool valid = id < P.E;
     ids_s[tid] = valid ? id : FULL;
@@ -576,6 +619,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mlp_down(const FewParams P) {
         experts[rank] = id;
         for (uint32_t t = 0; t < tid; t++) place += ids_s[t] == id;
     }
+    float *const ysm = (float *)(sm + FEW_WARPS * RING * STAGE);  // [warp][token][32]
+    for (uint32_t o = tid; o < FEW_WARPS * P.m * 32u; o += FEW_THREADS) ysm[o] = 0.f;
     __syncthreads();
     if (warp == 0) {
         uint32_t carry = 0;
@@ -593,26 +638,23 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mlp_down(const FewParams P) {
     }
     __syncthreads();
     if (valid) pairs[first[rank] + place] = tid;
+    __syncthreads();
 
     const uint32_t r = lane >> 2, q = lane & 3u;
     const uint32_t nu = P.I / 32u, steps = (nu + 3u) / 4u, row_bytes = P.I / 2u;
-    const uint32_t row0 = blockIdx.x * 16u;
-    const uint32_t srow = scale_bytes(KIND, P.g2), sslot = 16u * srow * (affine_kind<KIND> ? 2u : 1u);
-    // items: (expert, part of its steps), dealt to the warps in turn
-    const uint32_t parts = D == 0 || D % FEW_WARPS == 0 || D >= 32u
-                               ? 1u
-                               : tmin<uint32_t>(D >= FEW_WARPS ? 2u : FEW_WARPS / D, P.max_parts);
+    const uint32_t crank = P.cluster > 1u ? cluster_rank() : 0u, warps = P.cluster * FEW_WARPS;
+    const uint32_t row0 = blockIdx.x / P.cluster * 32u;
+    const uint32_t srow = scale_bytes(KIND, P.g2);
+    // about four items a warp
+    const uint32_t parts = D ? tmin<uint32_t>((4u * warps + D - 1u) / D, steps) : 1u;
     const uint32_t items = D * parts;
-    const uint32_t warp_bytes = P.stages * STAGE + P.slots * sslot;
-    uint8_t *const wsm = sm + warp * warp_bytes;
-    const uint32_t ring = ptx::smem_u32(wsm), sslots = ring + P.stages * STAGE;
-    float *const ysm = (float *)(sm + FEW_WARPS * warp_bytes);  // [warp][token][16]
-    for (uint32_t o = tid; o < FEW_WARPS * P.m * 16u; o += FEW_THREADS) ysm[o] = 0.f;
-    __syncthreads();
+    uint8_t *const wsm = sm + warp * RING * STAGE;
+    const uint32_t ring = ptx::smem_u32(wsm);
 
-    // a position in the warp's list of steps; x, j0: the item's expert and first step
+    // a position in the warp's list of steps: item, its first step, step, first pair of
+    // the pass and of the expert, pairs of the expert
     struct Pos {
-        uint32_t item, slot, x, j0, pb, j, cnt, first;
+        uint32_t item, x, j0, j, pb, first, cnt;
     };
     auto enter = [&](Pos &p) {
         if (p.item < items) {
@@ -623,109 +665,155 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mlp_down(const FewParams P) {
             p.cnt = first[p.x + 1u] - p.first;
         }
     };
-    auto advance = [&](Pos &p) {
+    auto advance = [&](Pos &p) {  // whether a pass ended
         p.j += parts;
         if (p.j < steps) return false;
         p.j = p.j0;
         p.pb += PP;
         if (p.pb >= p.cnt) {
-            p.item += FEW_WARPS;
-            p.slot = p.slot + 1u == P.slots ? 0u : p.slot + 1u;
+            p.item += warps;
             enter(p);
         }
-        return true;  // a pass ended
+        return true;
     };
+    // requests: the weights and their scales, then h
+    const uint8_t *w0 = nullptr, *s0 = nullptr, *b0 = nullptr;
+    auto start_w = [&](const Pos &p) {
+        if (p.item >= items) return;
+        const size_t row = (size_t)experts[p.x] * P.H + row0;
+        w0 = P.w2 + (row + r) * row_bytes + q * 16u;          // the lane's unit of row r, step 0
+        s0 = P.s2 + (row + lane) * srow;                      // scales: lane = row
+        if constexpr (affine_kind<KIND>) b0 = P.a2 + (row + lane) * srow;
+    };
+    // bytes of a step's scales in their row
+    const uint32_t sfirst = affine_kind<KIND> ? 0u : KIND == K_NVFP4 ? 8u : 4u;
+    auto scale_at = [&](uint32_t j) { return affine_kind<KIND> ? ((4u * j) >> P.gshift2) * 2u : sfirst * j; };
     auto issue_w = [&](const Pos &p, uint32_t stage) {
-        const uint32_t e = experts[p.x];
-        const size_t row = (size_t)e * P.H + row0;
-        const uint32_t u = 4u * p.j + q, size = u < nu ? 16u : 0u;
-        const uint8_t *src = P.w2 + (row + r) * row_bytes + (size ? u : 0u) * 16u;
-        const uint32_t st = ring + stage * STAGE + lane * 16u;
-        ptx::cp_async_16(st, src, size);
-        ptx::cp_async_16(st + 512u, src + 8u * row_bytes, size);
-        if (p.pb == 0u && p.j == p.j0) {  // first step of the item: its scales
-            const uint32_t ss = sslots + p.slot * sslot;
-            for (uint32_t o = lane * 16u; o < 16u * srow; o += 512u) {
-                ptx::cp_async_16(ss + o, P.s2 + row * srow + o, 16);
-                if constexpr (affine_kind<KIND>) ptx::cp_async_16(ss + 16u * srow + o, P.a2 + row * srow + o, 16);
+        const uint32_t size = 4u * p.j + q < nu ? 16u : 0u;
+        const uint8_t *src = w0 + (size ? p.j * 64u : 0u);
+        const uint32_t st = ring + stage + lane * 16u;
+#pragma unroll
+        for (uint32_t t = 0; t < 2 * TILES; t++) ptx::cp_async_16(st + t * 512u, src + t * 8u * row_bytes, size);
+        // the aligned words that hold bytes [o, end) of this lane's row
+        const uint32_t o = scale_at(p.j), end = tmin<uint32_t>(scale_at(p.j + 1u) + (P.gshift2 > 2u ? 2u : 0u), srow);
+        const uint32_t ss = ring + stage + WBYTES + PP * HSTEP + lane * DN_SROW;
+        const uint32_t off = (uint32_t)((uintptr_t)(s0 + o) & 3u);
+#pragma unroll
+        for (uint32_t k = 0; k < 3; k++)
+            if (o + 4u * k < end + off) {
+                ptx::cp_async_4(ss + 4u * k, s0 + o - off + 4u * k, 4);
+                if constexpr (affine_kind<KIND>) ptx::cp_async_4(ss + SBYTES + 4u * k, b0 + o - off + 4u * k, 4);
             }
-        }
+    };
+    uint32_t ho[PP];  // the pairs' offsets in hf
+    auto start_h = [&](const Pos &p) {
+        if (p.item >= items) return;
+#pragma unroll
+        for (uint32_t k = 0; k < PP; k++)
+            ho[k] = p.pb + k < p.cnt ? pairs[p.first + p.pb + k] * steps * HSTEP + lane * 16u : 0u;
     };
     auto issue_h = [&](const Pos &p, uint32_t stage) {
-        const uint32_t st = ring + stage * STAGE + WBYTES;
+        const uint32_t st = ring + stage + WBYTES + lane * 16u;
+        const uint8_t *src = P.hf + p.j * HSTEP;
 #pragma unroll
-        for (uint32_t k = 0; k < PP; k++) {
+        for (uint32_t k = 0; k < PP; k++)
             if (p.pb + k < p.cnt) {
-                const uint8_t *src = P.hf + ((size_t)pairs[p.first + p.pb + k] * steps + p.j) * HSTEP;
-                for (uint32_t o = lane * 16u; o < HSTEP; o += 512u) ptx::cp_async_16(st + k * HSTEP + o, src + o, 16);
+#pragma unroll
+                for (uint32_t o = 0; o < HSTEP; o += 512u)
+                    if (lane * 16u + o < HSTEP) ptx::cp_async_16(st + k * HSTEP + o, src + ho[k] + o, 16);
             }
-        }
     };
 
-    // `stages` steps ahead of the arithmetic, which P.slots covers: an item has at least
-    // steps / max_parts steps
-    Pos ahead{};
-    ahead.item = warp;
+    Pos ahead{crank * FEW_WARPS + warp, 0u, 0u, 0u, 0u, 0u, 0u};
     enter(ahead);
-    Pos at = ahead, fill = ahead;
+    Pos at = ahead;
+    start_w(ahead);
     uint32_t issued = 0;
-    while (issued < P.stages && ahead.item < items) {
-        issue_w(ahead, issued++);
-        advance(ahead);
+    for (; issued < RING && ahead.item < items; issued++) {
+        issue_w(ahead, issued * STAGE);
+        if (advance(ahead)) start_w(ahead);
     }
     ptx::cp_async_commit();
     ptx::griddep_wait();  // h
-    for (uint32_t i = 0; i < P.stages; i++) {
+    Pos fill = at;
+    start_h(fill);
+    for (uint32_t i = 0; i < RING; i++) {
         if (i < issued) {
-            issue_h(fill, i);
-            advance(fill);
+            issue_h(fill, i * STAGE);
+            if (advance(fill)) start_h(fill);
         }
         ptx::cp_async_commit();
     }
+    start_h(ahead);
 
-    float acc[NB][2];
+    float acc[TILES][NB][2];
 #pragma unroll
-    for (int n = 0; n < NB; n++) acc[n][0] = acc[n][1] = 0.f;
+    for (uint32_t t = 0; t < TILES; t++)
+#pragma unroll
+        for (int n = 0; n < NB; n++) acc[t][n][0] = acc[t][n][1] = 0.f;
     uint32_t stage = 0;
     while (at.item < items) {
-        wait_groups(P.stages - 1u);  // the oldest stage: its weights came in an older group
-        __syncwarp();                // and the other lanes' parts of the scales and of h
-        const uint8_t *st = wsm + stage * STAGE;
+        wait_groups<RING - 1>();  // the oldest step: its weights came in an older group
+        __syncwarp();             // and the other lanes' parts of the scales and of h
+        const uint8_t *st = wsm + stage;
         StepB<NB> B;
-        load_step<KIND, NPL, NB>(B, st + WBYTES, at.cnt - at.pb, lane);
-        const uint32_t u = 4u * at.j + 2u * (q & 1u);
-        const uint32_t u0 = tmin<uint32_t>(u, nu - 1u), u1 = tmin<uint32_t>(u + 1u, nu - 1u);
-        const uint8_t *ss = wsm + P.stages * STAGE + at.slot * sslot + r * srow;
-        tile_step<KIND, NB>(*(const uint4 *)(st + lane * 16u), *(const uint4 *)(st + 512u + lane * 16u), B, ss,
-                            ss + 8u * srow, ss + 16u * srow, ss + 24u * srow, u0, u1, P.gshift2, acc);
+        load_step<KIND, NPL, NB>(B, st + WBYTES, HSTEP, zeros, at.cnt - at.pb, lane);
+        // entries of the step's scales, from its first one; past the row they are the last
+        const uint32_t u = 2u * (q & 1u), last = nu - 1u - 4u * at.j;
+        uint32_t i0 = tmin<uint32_t>(u, last), i1 = tmin<uint32_t>(u + 1u, last);
+        if constexpr (affine_kind<KIND>) {
+            const uint32_t g = (4u * at.j) >> P.gshift2;
+            i0 = ((4u * at.j + i0) >> P.gshift2) - g;
+            i1 = ((4u * at.j + i1) >> P.gshift2) - g;
+        }
+        const uint8_t *ss = st + WBYTES + PP * HSTEP;
+        const uint32_t so = scale_at(at.j);
+#pragma unroll
+        for (uint32_t t = 0; t < TILES; t++) {
+            // a row's bytes stand at their own address modulo 4 (arrays and row0 * srow are multiples of 16)
+            const uint32_t ra = 16u * t + r, rb = ra + 8u;
+            const uint8_t *sa = ss + ra * DN_SROW + ((ra * srow + so) & 3u), *sb = ss + rb * DN_SROW + ((rb * srow + so) & 3u);
+            Scales<KIND> C;
+            load_scales<KIND>(C, sa, sb, sa + SBYTES, sb + SBYTES, i0, i1, P.gshift2 != 0u);
+            tile_step<KIND, NB>(*(const uint4 *)(st + t * 1024u + lane * 16u),
+                                *(const uint4 *)(st + t * 1024u + 512u + lane * 16u), B, C, acc[t]);
+        }
         const uint32_t pfirst = at.first + at.pb, pcnt = at.cnt - at.pb;
         const bool ended = advance(at);
-        __syncwarp();  // every lane has read its stage and scales
+        __syncwarp();  // every lane has read its stage
         if (ahead.item < items) {
             issue_w(ahead, stage);
             issue_h(ahead, stage);
-            advance(ahead);
+            if (advance(ahead)) {
+                start_w(ahead);
+                start_h(ahead);
+            }
         }
         ptx::cp_async_commit();
-        stage = stage + 1u == P.stages ? 0u : stage + 1u;
+        stage = stage + STAGE == RING * STAGE ? 0u : stage + STAGE;
         if (ended) {  // end of a pass: into the tokens' sums
 #pragma unroll
             for (uint32_t n = 0; n < NB; n++) {
-                float v[2];
+                float v[TILES][2];
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    v[h] = acc[n][h] + __shfl_xor_sync(FULL, acc[n][h], 1);
-                    if constexpr (NPL == 2) v[h] += __shfl_xor_sync(FULL, v[h], 2);
-                    acc[n][h] = 0.f;
-                }
+                for (uint32_t t = 0; t < TILES; t++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        v[t][h] = acc[t][n][h] + __shfl_xor_sync(FULL, acc[t][n][h], 1);
+                        if constexpr (NPL == 2) v[t][h] += __shfl_xor_sync(FULL, v[t][h], 2);
+                        acc[t][n][h] = 0.f;
+                    }
                 // one pair at a time: two of them may be one token's
 #pragma unroll
                 for (uint32_t k = 0; k < 2u / NPL; k++) {
                     const uint32_t p = n * (2u / NPL) + k;
                     if (q == 2u * k && p < pcnt) {
-                        float *y = ysm + ((size_t)warp * P.m + pairs[pfirst + p] / P.S) * 16u;
-                        y[r] += v[0];
-                        y[r + 8u] += v[1];
+                        float *y = ysm + ((size_t)warp * P.m + pairs[pfirst + p] / P.S) * 32u + r;
+#pragma unroll
+                        for (uint32_t t = 0; t < TILES; t++) {
+                            y[16u * t] += v[t][0];
+                            y[16u * t + 8u] += v[t][1];
+                        }
                     }
                     __syncwarp();
                 }
@@ -734,11 +822,23 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mlp_down(const FewParams P) {
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    for (uint32_t o = tid; o < P.m * 16u; o += FEW_THREADS) {
-        const uint32_t t = o >> 4, c = row0 + (o & 15u);
+    float *const bsum = (float *)sm;  // this block's sums [token][32], where the ring was
+    for (uint32_t o = tid; o < P.m * 32u; o += FEW_THREADS) {
         float y = 0.f;
 #pragma unroll
-        for (uint32_t w = 0; w < FEW_WARPS; w++) y += ysm[((size_t)w * P.m + t) * 16u + (o & 15u)];
+        for (uint32_t w = 0; w < FEW_WARPS; w++) y += ysm[w * P.m * 32u + o];
+        bsum[o] = y;
+    }
+    if (P.cluster > 1u) cluster_sync();
+    else __syncthreads();
+    const uint32_t baddr = ptx::smem_u32(bsum);
+    for (uint32_t o = crank * FEW_THREADS + tid; o < P.m * 32u; o += P.cluster * FEW_THREADS) {
+        const uint32_t t = o >> 5, c = row0 + (o & 31u);
+        float y = bsum[o];
+        if (P.cluster > 1u) {
+            y = 0.f;
+            for (uint32_t k = 0; k < P.cluster; k++) y += cluster_load(baddr + 4u * o, k);
+        }
         if (P.bias2)
             for (uint32_t s = 0; s < P.S; s++) {
                 const uint32_t e = ids_s[t * P.S + s];
@@ -754,19 +854,21 @@ __global__ void __launch_bounds__(FEW_THREADS, 2) mlp_down(const FewParams P) {
         }
         store_out(P.out, P.out_dtype, oi, y);
     }
+    if (P.cluster > 1u) cluster_sync();  // the other blocks have read this one's sums
 }
 
 // ------------------------------------------------------------------ launches
 
+// mlp_up's shared memory beside the ring: the pass's step images and the rows' scales.
+size_t up_fixed_bytes(int kind, uint32_t H, uint32_t groups, int x_dtype, uint32_t blocks) {
+    const int planes = x_planes(x_dtype);
+    return (size_t)(2u * blocks / planes) * ((H / 32u + 3u) / 4u) * step_bytes(planes) +
+           64ull * scale_bytes(kind, groups) * (kind == K_AFF4 ? 2u : 1u);
+}
+
 template <int KIND, int XT, int NB>
-cudaError_t up_t(FewParams P, cudaStream_t st) {
-    constexpr size_t stage = FEW_WARPS * UP_TILES * 2 * 512;
-    constexpr size_t image = FEW_WARPS * (2 * NB / x_planes(XT)) * step_bytes(x_planes(XT));
-    const size_t fixed = image + 64ull * scale_bytes(KIND, P.g1) * (KIND == K_AFF4 ? 2u : 1u);
-    // as deep as two CTAs an SM leave room for
-    const size_t room = fixed + 2 * stage <= FEW_SMEM_TWO ? FEW_SMEM_TWO : FEW_SMEM_ONE;
-    P.stages = fixed + 4 * stage <= room ? 4 : fixed + 3 * stage <= room ? 3 : 2;
-    const size_t smem = P.stages * stage + fixed;
+cudaError_t up_t(const FewParams &P, cudaStream_t st) {
+    const size_t smem = UP_RING + up_fixed_bytes(KIND, P.H, P.g1, XT, NB);
     auto kern = mlp_up<KIND, XT, NB>;
     static int smem_set[64];
     const cudaError_t e = ensure_dyn_smem(kern, smem, smem_set);
@@ -775,36 +877,36 @@ cudaError_t up_t(FewParams P, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+constexpr size_t down_bytes(bool affine, int planes, int blocks) {
+    return (size_t)FEW_WARPS * RING *
+           (TILES * 1024 + (2 * blocks / planes) * step_bytes(planes) + 32 * DN_SROW * (affine ? 2 : 1));
+}
+
 template <int KIND, int NPL, int NB>
 cudaError_t down_t(FewParams P, cudaStream_t st) {
-    constexpr size_t stage = 2 * 512 + (2 * NB / NPL) * step_bytes(NPL);
-    const size_t sslot = 16ull * scale_bytes(KIND, P.g2) * (KIND == K_AFF4 ? 2u : 1u);
-    const uint32_t steps = (P.I / 32u + 3u) / 4u;
-    P.max_parts = steps / 3u ? steps / 3u : 1u;
-    const uint32_t least = steps / P.max_parts;  // steps of an item
-    size_t smem = 0;
-    for (uint32_t stages = 8;; stages -= 2) {
-        P.stages = stages;
-        P.slots = stages / least + 2u;
-        smem = FEW_WARPS * (P.stages * stage + P.slots * sslot) + 512ull * P.m;
-        if (smem <= FEW_SMEM_TWO || stages == 4u) break;
-    }
+    const size_t smem = down_bytes(affine_kind<KIND>, NPL, NB) + FEW_WARPS * 128ull * P.m;
     auto kern = mlp_down<KIND, NPL, NB>;
     static int smem_set[64];
     const cudaError_t e = ensure_dyn_smem(kern, smem, smem_set);
     if (e != cudaSuccess) return e;
+    // blocks for two an SM or more, so that the SMs' shares are even
+    P.cluster = 1u;
+    while (P.cluster < 8u && P.H / 32u * P.cluster < 2u * 148u) P.cluster *= 2u;
     // a programmatic dependent of mlp_up: it requests its weights while mlp_up runs and
     // waits (griddepcontrol.wait) before it reads h
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(P.H / 16u);
+    cfg.gridDim = dim3(P.H / 32u * P.cluster);
     cfg.blockDim = dim3(FEW_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = P.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, P);
 }
 
@@ -818,7 +920,9 @@ uint32_t blocks_a_pass(const FewParams &P, uint32_t planes) {
 
 template <int KIND, int XT>
 cudaError_t up_x(const FewParams &P, cudaStream_t st) {
-    switch (blocks_a_pass(P, x_planes(XT))) {
+    uint32_t blocks = blocks_a_pass(P, x_planes(XT));
+    while (blocks > 1u && up_fixed_bytes(KIND, P.H, P.g1, XT, blocks) + UP_RING > FEW_SMEM) blocks /= 2u;
+    switch (blocks) {
         case 1: return up_t<KIND, XT, 1>(P, st);
         case 2: return up_t<KIND, XT, 2>(P, st);
         default: return up_t<KIND, XT, 4>(P, st);
@@ -834,7 +938,10 @@ cudaError_t up_k(const FewParams &P, cudaStream_t st) {
 
 template <int KIND, int NPL>
 cudaError_t down_p(const FewParams &P, cudaStream_t st) {
-    switch (blocks_a_pass(P, NPL)) {
+    uint32_t blocks = blocks_a_pass(P, NPL);
+    while (blocks > 1u && down_bytes(affine_kind<KIND>, NPL, (int)blocks) + FEW_WARPS * 128ull * P.m > FEW_SMEM)
+        blocks /= 2u;
+    switch (blocks) {
         case 1: return down_t<KIND, NPL, 1>(P, st);
         case 2: return down_t<KIND, NPL, 2>(P, st);
         default: return down_t<KIND, NPL, 4>(P, st);
@@ -871,7 +978,7 @@ uint64_t mlp_few_workspace(uint32_t m, uint32_t inter, uint32_t S) {
 }
 
 // Whole 32-code units of 16 aligned bytes and scale groups of whole units in both
-// projections, at most 256 pairs of at most 64 tokens, scales of a CTA's rows that fit
+// projections, at most 256 pairs of at most 64 tokens, x and the scales of a CTA's rows
 // in shared memory beside the ring.
 bool mlp_few_supported(const MlpArgs &a) {
     const uint64_t R = (uint64_t)a.m * a.S;
@@ -880,12 +987,10 @@ bool mlp_few_supported(const MlpArgs &a) {
     if ((uintptr_t)a.x & 15u) return false;
     const int k1 = kind_of((int)a.gate_up->fmt, (int)a.gate_up->bits);
     const int k2 = kind_of((int)a.down->fmt, (int)a.down->bits);
-    const size_t sc1 = 64ull * scale_bytes(k1, a.hidden / a.gate_up->group_size) * (k1 == K_AFF4 ? 2u : 1u);
-    const size_t sc2 = 16ull * scale_bytes(k2, a.inter / a.down->group_size) * (k2 == K_AFF4 ? 2u : 1u);
-    // the least that the widest variants need: two stages; four stages, six experts' scales
-    const size_t up = FEW_WARPS * (2ull * UP_TILES * 1024 + 8ull * step_bytes(1)) + sc1;
-    const size_t dn = FEW_WARPS * (4ull * (1024 + 8ull * step_bytes(1)) + 6ull * sc2) + 512ull * a.m;
-    return up <= FEW_SMEM_ONE && dn <= FEW_SMEM_ONE;
+    // both with one block of columns
+    const size_t up = UP_RING + up_fixed_bytes(k1, a.hidden, a.hidden / a.gate_up->group_size, a.x_dtype, 1);
+    const size_t dn = down_bytes(k2 == K_AFF4, 1, 1) + FEW_WARPS * 128ull * a.m;
+    return up <= FEW_SMEM && dn <= FEW_SMEM;
 }
 
 cudaError_t launch_mlp_few(const MlpArgs &a, uint32_t *err, void *hf, cudaStream_t st) {
