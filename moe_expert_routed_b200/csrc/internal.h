@@ -145,7 +145,7 @@ struct MlpArgs {
 };
 // The two kernels for few tokens: what they take, the bytes of h's planes, the launch.
 bool mlp_few_supported(const MlpArgs &a);
-uint64_t mlp_few_workspace(uint32_t m, uint32_t inter, uint32_t S);
+uint64_t mlp_few_workspace(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t S);
 cudaError_t launch_mlp_few(const MlpArgs &a, uint32_t *err, void *hf, cudaStream_t st);
 
 // moe_qmm_id's scalar validation (MOE_OK or the status moe_qmm_id would return).

@@ -28,7 +28,7 @@ bool layout(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t S, uint32_t E,
     const uint64_t R = (uint64_t)m * S;
     if (R > 0x7FFFFFFFull) return false;
     const moe_dtype hd = h_dtype(x_dtype);
-    const uint64_t few = mlp_few_workspace(m, inter, S);
+    const uint64_t few = mlp_few_workspace(m, hidden, inter, S);
     const size_t a = moe_qmm_id_workspace_bytes_k(m, hidden, S, E, (moe_dtype)x_dtype);
     const size_t b = moe_qmm_id_workspace_bytes_k((uint32_t)R, inter, 1, E, hd);
     if (!a || !b) return false;
