@@ -146,26 +146,29 @@ __host__ __device__ constexpr uint32_t scale_bytes(bool aff, uint32_t groups) { 
 // ------------------------------------------------------------------ one step
 
 // Where a lane reads its part of the step images (shared addresses): for each block of
-// columns the B registers and the factors and sums of its accumulator columns; the
-// lanes whose k are not their column's unit, and pairs past the last, read zeros.
+// columns the B registers, with `move` all ones where they move with the step, and the
+// factors and sums of its accumulator columns. The lanes whose k are not their column's
+// unit read zeros. Pairs past a pass's last are not masked: their columns hold what the
+// memory holds, mix with no other column and are dropped.
 template <int NB>
 struct StepAt {
-    uint32_t b[NB], f[NB];
+    uint32_t b[NB], f[NB], move;
 };
 
 template <int PLANES, int NB>
-__device__ __forceinline__ void step_at(StepAt<NB> &A, uint32_t base, uint32_t stride, uint32_t zeros, uint32_t np,
-                                        uint32_t lane) {
+__device__ __forceinline__ StepAt<NB> step_at(uint32_t base, uint32_t stride, uint32_t zeros, uint32_t lane) {
+    StepAt<NB> A;
     const uint32_t q = lane & 3u;
     const bool active = ((lane >> 2) & 3u) == q;  // this lane's k of column lane / 4 are that column's unit
+    A.move = active ? FULL : 0u;
 #pragma unroll
     for (uint32_t n = 0; n < NB; n++) {
         const uint32_t set = 2u * n + (lane >> 4), pair = set / PLANES, plane = set % PLANES;
-        A.b[n] = active && pair < np ? base + pair * stride + plane * 256u + q * 64u : zeros;
+        A.b[n] = active ? base + pair * stride + plane * 256u + q * 64u : zeros;
         // accumulator columns 2q, 2q + 1: units 2 (q mod 2) and the next of set 2n + q / 2
-        const uint32_t cpair = (2u * n + (q >> 1)) / PLANES;
-        A.f[n] = cpair < np ? base + cpair * stride + PLANES * 256u + (q & 1u) * 16u : zeros;
+        A.f[n] = base + (2u * n + (q >> 1)) / PLANES * stride + PLANES * 256u + (q & 1u) * 16u;
     }
+    return A;
 }
 
 // Scales (and affine biases) that a lane applies: of rows r and r + 8 and the two units of
@@ -249,10 +252,11 @@ __device__ __forceinline__ void tile_step(const uint4 wa, const uint4 wb, const 
 }
 
 // One step of T tiles: st the stage's address for this lane (+ 16 lane), sc that of row r's
-// scales of the first tile (tot bytes on to the next tile's), at the step images.
+// scales of the first tile (tot bytes on to the next tile's), `on` bytes past at the images.
 template <int MODE, int PLANES, int NB, int T>
 __device__ __forceinline__ void step(uint32_t st, uint32_t sc, uint32_t tot, uint32_t to8, uint32_t tob, uint32_t i,
-                                     uint32_t d, const StepAt<NB> &at, uint32_t lane, float (&acc)[T][NB][2]) {
+                                     uint32_t d, const StepAt<NB> &at, uint32_t on, uint32_t lane,
+                                     float (&acc)[T][NB][2]) {
     uint32_t B[NB][16];
     float f[NB][2], xs[NB][2];
     const bool odd_plane = PLANES == 2 && (lane & 2u);
@@ -261,10 +265,10 @@ __device__ __forceinline__ void step(uint32_t st, uint32_t sc, uint32_t tot, uin
     for (int n = 0; n < NB; n++) {
 #pragma unroll
         for (int k = 0; k < 4; k++) {
-            const uint4 v = lds128(at.b[n] + 16u * k);
+            const uint4 v = lds128(at.b[n] + (on & at.move) + 16u * k);
             B[n][4 * k] = v.x; B[n][4 * k + 1] = v.y; B[n][4 * k + 2] = v.z; B[n][4 * k + 3] = v.w;
         }
-        const uint4 v = lds128(at.f[n]);
+        const uint4 v = lds128(at.f[n] + on);
         f[n][0] = __uint_as_float(v.x) * unit;
         f[n][1] = __uint_as_float(v.z) * unit;
         xs[n][0] = odd_plane ? 0.f : __uint_as_float(v.y);  // the bias once a pair
@@ -512,14 +516,8 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const Few
         wait_groups<RING - 1>();  // the first unit's scales came with the first step
         __syncthreads();          // images, scales
 
-        StepAt<NB> first, hop;  // hop: to the warp's next step; 0 on zeros
-        step_at<PLANES, NB>(first, ptx::smem_u32(images) + part * XSTEP, steps * XSTEP, ptx::smem_u32(zeros), npass,
-                            lane);
-#pragma unroll
-        for (int n = 0; n < NB; n++) {
-            hop.b[n] = first.b[n] == ptx::smem_u32(zeros) ? 0u : UP_PARTS * XSTEP;
-            hop.f[n] = first.f[n] == ptx::smem_u32(zeros) ? 0u : UP_PARTS * XSTEP;
-        }
+        const StepAt<NB> at =
+            step_at<PLANES, NB>(ptx::smem_u32(images) + part * XSTEP, steps * XSTEP, ptx::smem_u32(zeros), lane);
         uint32_t slot = 0, buf = 0;
         for (uint32_t unit = blockIdx.x; unit < units; unit += gridDim.x, buf ^= 1u) {
             float acc[UP_TILES][NB][2];
@@ -527,7 +525,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const Few
             for (uint32_t t = 0; t < UP_TILES; t++)
 #pragma unroll
                 for (int n = 0; n < NB; n++) acc[t][n][0] = acc[t][n][1] = 0.f;
-            StepAt<NB> at = first;
+            uint32_t on = 0;
             const uint32_t sc = sc0 + buf * sbytes + (16u * tp + r) * srow;
             issue_scales(unit + gridDim.x, buf ^ 1u);  // with this unit's first step
             for (uint32_t j = part; j < steps; j += UP_PARTS) {
@@ -535,12 +533,8 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const Few
                 const uint32_t u0 = tmin<uint32_t>(4u * j + 2u * (q & 1u), nu - 1u), u1 = tmin<uint32_t>(u0 + 1u, nu - 1u);
                 const uint32_t i = scale_entry<MODE>(u0, P.gshift1);
                 step<MODE, PLANES, NB, UP_TILES>(ring + slot + lane * 16u, sc, 8u * srow, sblock, 2u * sblock, i,
-                                                 scale_entry<MODE>(u1, P.gshift1) - i, at, lane, acc);
-#pragma unroll
-                for (int n = 0; n < NB; n++) {
-                    at.b[n] += hop.b[n];
-                    at.f[n] += hop.f[n];
-                }
+                                                 scale_entry<MODE>(u1, P.gshift1) - i, at, on, lane, acc);
+                on += UP_PARTS * XSTEP;
                 slot = slot + STAGE == RING * STAGE ? 0u : slot + STAGE;
                 issue();
                 ptx::cp_async_commit();
@@ -607,15 +601,15 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const Few
     }
 }
 
-// mlp_down. grid (hidden / 16, split): a CTA holds 16 columns of out, `split` CTAs share
-// them. Their warps share the work items, (expert, part of its steps); each keeps sums of
+// mlp_down. grid (hidden / (16 T), split): a CTA holds T tiles, 16 T columns of out, and
+// `split` CTAs share them. Their warps share the work items, (expert, part of its steps); each keeps sums of
 // its own for every token, added in warp order, and with a split the last CTA to arrive
 // adds the CTAs' sums in their order: no float atomics, one order. Weights and scales do
 // not depend on mlp_up, so the ring's first steps are requested before waiting for it.
-template <int MODE, int NPL, int NB>
+template <int MODE, int NPL, int NB, int T>
 __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const FewParams P) {
-    constexpr uint32_t PP = 2 * NB / NPL;  // pairs a pass
-    constexpr uint32_t HSTEP = step_bytes(NPL), HAT = 2 * 512, STAGE = HAT + PP * HSTEP;
+    constexpr uint32_t PP = 2 * NB / NPL, C = 16 * T;  // pairs a pass, columns
+    constexpr uint32_t HSTEP = step_bytes(NPL), HAT = T * 2 * 512, STAGE = HAT + PP * HSTEP;
     extern __shared__ __align__(16) uint8_t sm[];
     __shared__ __align__(16) uint8_t zeros[64];
     __shared__ uint32_t mask[32], base[33], ids_s[FEW_MAX_R], first[FEW_MAX_R + 1], pairs[FEW_MAX_R],
@@ -637,10 +631,10 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const F
         experts[rank] = id;
         for (uint32_t t = 0; t < tid; t++) place += ids_s[t] == id;
     }
-    const uint32_t srow = scale_bytes(affine(MODE), P.g2), sslot = 16u * srow * (affine(MODE) ? 2u : 1u);
+    const uint32_t srow = scale_bytes(affine(MODE), P.g2), sslot = C * srow * (affine(MODE) ? 2u : 1u);
     const uint32_t warp_bytes = RING * STAGE + P.slots * sslot;
-    float *const ysm = (float *)(sm + FEW_WARPS * warp_bytes);  // [warp][token][16]
-    for (uint32_t o = tid; o < FEW_WARPS * P.m * 16u; o += FEW_THREADS) ysm[o] = 0.f;
+    float *const ysm = (float *)(sm + FEW_WARPS * warp_bytes);  // [warp][token][C]
+    for (uint32_t o = tid; o < FEW_WARPS * P.m * C; o += FEW_THREADS) ysm[o] = 0.f;
     __syncthreads();
     if (warp == 0) {
         uint32_t carry = 0;
@@ -662,9 +656,9 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const F
 
     const uint32_t r = lane >> 2, q = lane & 3u;
     const uint32_t nu = P.I / 32u, steps = (nu + 3u) / 4u, row_bytes = P.I / 2u;
-    const uint32_t row0 = blockIdx.x * 16u, warps = P.split * FEW_WARPS;
-    // about four items a warp, or one where the experts fill the warps evenly
-    const uint32_t parts = D == 0u || D % warps == 0u ? 1u : tmin<uint32_t>((4u * warps + D - 1u) / D, P.max_parts);
+    const uint32_t row0 = blockIdx.x * C, warps = P.split * FEW_WARPS;
+    // an expert is one item where there are enough for the warps
+    const uint32_t parts = D == 0u || D >= warps ? 1u : tmin<uint32_t>((warps + D - 1u) / D, P.max_parts);
     const uint32_t ring = ptx::smem_u32(sm) + warp * warp_bytes, sslots = ring + RING * STAGE;
     const uint32_t dx = warps / parts, dp = warps - dx * parts;  // to a warp's next item: experts, parts
 
@@ -706,9 +700,9 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const F
         w0 = P.w2 + (row + r) * row_bytes + q * 16u;  // the lane's unit of row r, step 0
         if (p.pb == 0u) {
             const uint8_t *s = P.s2 + row * srow, *b = P.a2 + row * srow;
-            for (uint32_t o = lane * 16u; o < 16u * srow; o += 512u) {
+            for (uint32_t o = lane * 16u; o < C * srow; o += 512u) {
                 ptx::cp_async_16(sslots + p.slot + o, s + o, 16);
-                if constexpr (affine(MODE)) ptx::cp_async_16(sslots + p.slot + 16u * srow + o, b + o, 16);
+                if constexpr (affine(MODE)) ptx::cp_async_16(sslots + p.slot + C * srow + o, b + o, 16);
             }
         }
     };
@@ -716,8 +710,8 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const F
         const uint32_t size = 4u * p.j + q < nu ? 16u : 0u;
         const uint8_t *src = w0 + (size ? p.j * 64u : 0u);
         const uint32_t st = ring + stage + lane * 16u;
-        ptx::cp_async_16(st, src, size);
-        ptx::cp_async_16(st + 512u, src + 8u * row_bytes, size);
+#pragma unroll
+        for (uint32_t t = 0; t < 2 * T; t++, src += 8u * row_bytes) ptx::cp_async_16(st + t * 512u, src, size);
     };
     uint32_t ho[PP];  // the pairs' offsets in hf
     auto start_h = [&](const Pos &p) {
@@ -731,11 +725,9 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const F
         const uint8_t *src = P.hf + p.j * HSTEP;
 #pragma unroll
         for (uint32_t k = 0; k < PP; k++)
-            if (p.pb + k < p.cnt) {
 #pragma unroll
-                for (uint32_t o = 0; o < HSTEP; o += 512u)
-                    if (lane * 16u + o < HSTEP) ptx::cp_async_16(st + k * HSTEP + o, src + ho[k] + o, 16);
-            }
+            for (uint32_t o = 0; o < HSTEP; o += 512u)
+                ptx::cp_async_16_if(p.pb + k < p.cnt && lane * 16u + o < HSTEP, st + k * HSTEP + o, src + ho[k] + o, 16);
     };
 
     Pos ahead{};
@@ -766,19 +758,20 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const F
     }
     start_h(ahead);
 
-    float acc[1][NB][2];
+    float acc[T][NB][2];
 #pragma unroll
-    for (int n = 0; n < NB; n++) acc[0][n][0] = acc[0][n][1] = 0.f;
+    for (int t = 0; t < T; t++)
+#pragma unroll
+        for (int n = 0; n < NB; n++) acc[t][n][0] = acc[t][n][1] = 0.f;
+    const StepAt<NB> sa = step_at<NPL, NB>(ring + HAT, HSTEP, ptx::smem_u32(zeros), lane);
     uint32_t stage = 0;
     while (at.x < D) {
         wait_groups<RING - 1>();  // the oldest step: its weights came in an older group
         __syncwarp();             // and the other lanes' parts of the scales and of h
-        StepAt<NB> sa;
-        step_at<NPL, NB>(sa, ring + stage + HAT, HSTEP, ptx::smem_u32(zeros), at.cnt - at.pb, lane);
         const uint32_t u0 = tmin<uint32_t>(4u * at.j + 2u * (q & 1u), nu - 1u), u1 = tmin<uint32_t>(u0 + 1u, nu - 1u);
         const uint32_t i = scale_entry<MODE>(u0, P.gshift2);
-        step<MODE, NPL, NB, 1>(ring + stage + lane * 16u, sslots + at.slot + r * srow, 0u, 8u * srow, 16u * srow, i,
-                               scale_entry<MODE>(u1, P.gshift2) - i, sa, lane, acc);
+        step<MODE, NPL, NB, T>(ring + stage + lane * 16u, sslots + at.slot + r * srow, 16u * srow, 8u * srow, C * srow, i,
+                               scale_entry<MODE>(u1, P.gshift2) - i, sa, stage, lane, acc);
         const uint32_t pfirst = at.first + at.pb, pcnt = at.cnt - at.pb;
         const bool ended = advance(at);
         __syncwarp();  // every lane has read its stage and scales
@@ -795,23 +788,30 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const F
         if (ended) {  // end of a pass: into the tokens' sums
 #pragma unroll
             for (uint32_t n = 0; n < NB; n++) {
-                float v[2];
+                float v[T][2];
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    v[h] = acc[0][n][h] + __shfl_xor_sync(FULL, acc[0][n][h], 1);
-                    if constexpr (NPL == 2) v[h] += __shfl_xor_sync(FULL, v[h], 2);
-                    acc[0][n][h] = 0.f;
-                }
+                for (int t = 0; t < T; t++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        v[t][h] = acc[t][n][h] + __shfl_xor_sync(FULL, acc[t][n][h], 1);
+                        if constexpr (NPL == 2) v[t][h] += __shfl_xor_sync(FULL, v[t][h], 2);
+                        acc[t][n][h] = 0.f;
+                    }
                 // one pair at a time: two of them may be one token's
 #pragma unroll
                 for (uint32_t k = 0; k < 2u / NPL; k++) {
                     const uint32_t p = n * (2u / NPL) + k;
-                    if (q == 2u * k && p < pcnt) {
-                        float *y = ysm + (warp * P.m + (pairs[pfirst + p] >> 16)) * 16u + r;
-                        y[0] += v[0];
-                        y[8] += v[1];
+                    if (p < pcnt) {
+                        if (q == 2u * k) {
+                            float *y = ysm + (warp * P.m + (pairs[pfirst + p] >> 16)) * C + r;
+#pragma unroll
+                            for (int t = 0; t < T; t++) {
+                                y[16 * t] += v[t][0];
+                                y[16 * t + 8] += v[t][1];
+                            }
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
             }
         }
@@ -822,12 +822,12 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const F
     auto own_sum = [&](uint32_t o) {
         float y = 0.f;
 #pragma unroll
-        for (uint32_t w = 0; w < FEW_WARPS; w++) y += ysm[w * P.m * 16u + o];
+        for (uint32_t w = 0; w < FEW_WARPS; w++) y += ysm[w * P.m * C + o];
         return y;
     };
     if (P.split > 1u) {
-        for (uint32_t o = tid; o < P.m * 16u; o += FEW_THREADS)
-            P.partial[((size_t)blockIdx.y * P.m + (o >> 4)) * P.H + row0 + (o & 15u)] = own_sum(o);
+        for (uint32_t o = tid; o < P.m * C; o += FEW_THREADS)
+            P.partial[((size_t)blockIdx.y * P.m + o / C) * P.H + row0 + o % C] = own_sum(o);
         __threadfence();
         __syncthreads();
         if (tid == 0) last_s = atomicAdd(&P.arrived[blockIdx.x], 1u) + 1u == P.split;
@@ -835,8 +835,8 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const F
         if (!last_s) return;
         __threadfence();
     }
-    for (uint32_t o = tid; o < P.m * 16u; o += FEW_THREADS) {
-        const uint32_t t = o >> 4, c = row0 + (o & 15u);
+    for (uint32_t o = tid; o < P.m * C; o += FEW_THREADS) {
+        const uint32_t t = o / C, c = row0 + o % C;
         const size_t oi = (size_t)t * P.H + c;
         float y = 0.f;
         if (P.split > 1u)
@@ -870,10 +870,10 @@ size_t up_bytes(bool aff, uint32_t H, uint32_t groups, int planes, uint32_t bloc
 // mlp_down: an item has steps / max_parts steps or more; RING steps ahead reach so many more.
 uint32_t down_parts(uint32_t steps) { return steps >= 4u ? steps / 2u : 1u; }
 uint32_t down_slots(uint32_t steps) { return RING / (steps / down_parts(steps)) + 2u; }
-size_t down_bytes(bool aff, uint32_t I, uint32_t groups, int planes, uint32_t blocks, uint32_t m) {
-    return FEW_WARPS * (RING * (1024ull + (2u * blocks / planes) * step_bytes(planes)) +
-                        down_slots((I / 32u + 3u) / 4u) * 16ull * scale_bytes(aff, groups) * (aff ? 2u : 1u)) +
-           FEW_WARPS * 64ull * m;
+size_t down_bytes(bool aff, uint32_t I, uint32_t groups, int planes, uint32_t blocks, uint32_t tiles, uint32_t m) {
+    return FEW_WARPS * (RING * (1024ull * tiles + (2u * blocks / planes) * step_bytes(planes)) +
+                        down_slots((I / 32u + 3u) / 4u) * 16ull * tiles * scale_bytes(aff, groups) * (aff ? 2u : 1u) +
+                        64ull * tiles * m);
 }
 
 template <int MODE, int PLANES, int NB>
@@ -891,10 +891,10 @@ cudaError_t up_t(const FewParams &P, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <int MODE, int NPL, int NB>
+template <int MODE, int NPL, int NB, int T>
 cudaError_t down_t(FewParams P, cudaStream_t st) {
-    const size_t smem = down_bytes(affine(MODE), P.I, P.g2, NPL, NB, P.m);
-    auto kern = mlp_down<MODE, NPL, NB>;
+    const size_t smem = down_bytes(affine(MODE), P.I, P.g2, NPL, NB, T, P.m);
+    auto kern = mlp_down<MODE, NPL, NB, T>;
     static int smem_set[64];
     const cudaError_t e = ensure_dyn_smem(kern, smem, smem_set);
     if (e != cudaSuccess) return e;
@@ -904,7 +904,7 @@ cudaError_t down_t(FewParams P, cudaStream_t st) {
     // a programmatic dependent of mlp_up: it requests its weights while mlp_up runs and
     // waits (griddepcontrol.wait) before it reads h
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(P.H / 16u, P.split);
+    cfg.gridDim = dim3(P.H / (16u * T), P.split);
     cfg.blockDim = dim3(FEW_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -937,12 +937,15 @@ cudaError_t up_p(const FewParams &P, cudaStream_t st) {
 
 template <int MODE, int NPL>
 cudaError_t down_p(const FewParams &P, cudaStream_t st) {
+    // a single token's columns on as many SMs as there are; else two tiles a warp, which
+    // share a step's B registers and its loop
+    if (P.split == 1u) return down_t<MODE, NPL, 1, 1>(P, st);
     uint32_t blocks = blocks_a_pass(P, NPL);
-    while (blocks > 1u && down_bytes(affine(MODE), P.I, P.g2, NPL, blocks, P.m) > FEW_SMEM) blocks /= 2u;
+    while (blocks > 1u && down_bytes(affine(MODE), P.I, P.g2, NPL, blocks, 2, P.m) > FEW_SMEM) blocks /= 2u;
     switch (blocks) {
-        case 1: return down_t<MODE, NPL, 1>(P, st);
-        case 2: return down_t<MODE, NPL, 2>(P, st);
-        default: return down_t<MODE, NPL, 4>(P, st);
+        case 1: return down_t<MODE, NPL, 1, 2>(P, st);
+        case 2: return down_t<MODE, NPL, 2, 2>(P, st);
+        default: return down_t<MODE, NPL, 4, 2>(P, st);
     }
 }
 
@@ -998,7 +1001,8 @@ bool mlp_few_supported(const MlpArgs &a) {
     const int m1 = mode_of(*a.gate_up, a.hidden), m2 = mode_of(*a.down, a.inter);
     if (m1 < 0 || m2 < 0 || ((uintptr_t)a.x & 15u)) return false;
     return up_bytes(affine(m1), a.hidden, a.hidden / a.gate_up->group_size, x_planes(a.x_dtype), 1) <= FEW_SMEM &&
-           down_bytes(affine(m2), a.inter, a.inter / a.down->group_size, h_planes(a.out_dtype), 1, a.m) <= FEW_SMEM;
+           down_bytes(affine(m2), a.inter, a.inter / a.down->group_size, h_planes(a.out_dtype), 1, 2, a.m) <=
+               FEW_SMEM;
 }
 
 cudaError_t launch_mlp_few(const MlpArgs &a, uint32_t *err, void *hf, cudaStream_t st) {
@@ -1022,7 +1026,7 @@ cudaError_t launch_mlp_few(const MlpArgs &a, uint32_t *err, void *hf, cudaStream
     P.down_affine = affine(m2);
     // CTAs enough for even shares of the SMs, where the work outweighs the join
     P.split = 1u;
-    while (P.R > 16u && P.split < MAX_SPLIT && P.H / 16u * P.split < 5u * 148u / 2u) P.split *= 2u;
+    if (P.R > 16u) P.split = P.H / 32u * 2u >= 5u * 148u / 2u ? 2u : MAX_SPLIT;
     const cudaError_t ce = m1 == M_AFF    ? up_m<M_AFF>(P, st)
                            : m1 == M_AFF1 ? up_m<M_AFF1>(P, st)
                            : m1 == M_NV   ? up_m<M_NV>(P, st)

@@ -145,6 +145,14 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, uint3
                  : "memory");
 }
 
+// The same where `on` is non-zero, nothing otherwise (a predicate, no branch).
+__device__ __forceinline__ void cp_async_16_if(uint32_t on, uint32_t dst, const void *src, uint32_t src_bytes) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(dst),
+        "l"(src), "r"(src_bytes), "r"(on)
+        : "memory");
+}
+
 // 4- and 8-byte copies (through L1); same zero-fill rule.
 __device__ __forceinline__ void cp_async_8(uint32_t dst, const void *src, uint32_t src_bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
