@@ -15,7 +15,6 @@ tensor is not on a CUDA device, calls raise.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -99,7 +98,7 @@ def lib() -> ctypes.CDLL:
         L.moe_gate_topk.restype = i32
         L.moe_combine.argtypes = [vp] * 5 + [u32] * 4 + [i32, i32, vp]
         L.moe_combine.restype = i32
-        L.moe_mlp.argtypes = [vp] * 7 + [u32] * 5 + [i32] * 3 + [vp, sz, vp, i32]
+        L.moe_mlp.argtypes = [vp] * 7 + [u32] * 5 + [i32] * 3 + [vp, sz, i32, vp]
         L.moe_mlp.restype = i32
         L.moe_mlp_workspace_bytes.argtypes = [u32] * 5 + [i32]
         L.moe_mlp_workspace_bytes.restype = sz
@@ -142,7 +141,13 @@ def new_workspace(m: int, n_expert_used: int, num_experts: int, device="cuda", k
     return torch.zeros(nbytes, dtype=torch.uint8, device=device)
 
 
+# The current stream's handle without building a torch.cuda.Stream (2.4 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_ptr(device) -> int:
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
@@ -456,14 +461,21 @@ def qmm_id_w4a4(x: torch.Tensor, ids: torch.Tensor, packed: torch.Tensor, scales
 # ----------------------------------------------------------- the layer around it
 
 
-def _on_device(device):
-    """The tensors' device made current for a launch (their stream belongs to it)."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _launch(device, fn, *args) -> int:
+    """Calls a C entry whose last argument is the stream, with the tensors' device current
+    (their stream belongs to it)."""
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, _stream_ptr(device))
+    with torch.cuda.device(device):
+        return fn(*args, _stream_ptr(device))
 
 
 def _want(t, what: str, shape: tuple, device, dtypes):
     """One tensor argument's checks: a contiguous CUDA tensor on `device` of one of
     the types and exactly this shape."""
+    if isinstance(t, torch.Tensor) and t.device == device and t.dtype in dtypes and t.shape == shape and \
+            t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a torch.Tensor")
     if not t.is_cuda or t.device != device:
@@ -514,10 +526,9 @@ def gate_topk(logits: torch.Tensor, top_k: int, *, score: str = "softmax",
         _want(weights, "gate_topk: weights", (m, top_k), device, _F32)
     if m == 0:
         return ids, weights
-    with _on_device(device):
-        st = lib().moe_gate_topk(logits.data_ptr(), select_bias.data_ptr() if select_bias is not None else None,
-                                 ids.data_ptr(), weights.data_ptr(), m, E, top_k, _TORCH_DT[logits.dtype],
-                                 _SCORES[score], 1 if renormalize else 0, scale, _stream_ptr(device))
+    st = _launch(device, lib().moe_gate_topk, logits.data_ptr(),
+                 select_bias.data_ptr() if select_bias is not None else None, ids.data_ptr(), weights.data_ptr(), m, E,
+                 top_k, _TORCH_DT[logits.dtype], _SCORES[score], 1 if renormalize else 0, scale)
     if st != MOE_OK:
         raise MoeError(st, "moe_gate_topk")
     return ids, weights
@@ -558,10 +569,9 @@ def combine(z: torch.Tensor, weights: torch.Tensor, *, ids: torch.Tensor | None 
         return out
     if S == 0 or n == 0:
         raise ValueError("combine: n_expert_used and n must be > 0")
-    with _on_device(device):
-        st = lib().moe_combine(z.data_ptr(), weights.data_ptr(), ids.data_ptr() if ids is not None else None,
-                               residual.data_ptr() if residual is not None else None, out.data_ptr(), m, S, n,
-                               num_experts or 0, _TORCH_DT[z.dtype], _TORCH_DT[out.dtype], _stream_ptr(device))
+    st = _launch(device, lib().moe_combine, z.data_ptr(), weights.data_ptr(),
+                 ids.data_ptr() if ids is not None else None, residual.data_ptr() if residual is not None else None,
+                 out.data_ptr(), m, S, n, num_experts or 0, _TORCH_DT[z.dtype], _TORCH_DT[out.dtype])
     if st != MOE_OK:
         raise MoeError(st, "moe_combine")
     return out
@@ -634,7 +644,7 @@ class MoeMlp:
             _check_dev(workspace, "workspace", device)
             if _nbytes(workspace) < need:
                 raise ValueError(f"MoeMlp: workspace too small: {need} bytes needed, got {_nbytes(workspace)}")
-        self.workspace, self.device, self.path = workspace, device, path
+        self.workspace, self.device = workspace, device
         self.hidden, self.n_expert_used, self.max_tokens = hidden, n_expert_used, max_tokens
         self.x_dtype, self.out_dtype = x_dtype, out_dtype
         self._weights = (gate_up, down)  # keeps the arrays alive
@@ -642,7 +652,7 @@ class MoeMlp:
         self._call = lib().moe_mlp
         self._ptrs = tuple(ctypes.addressof(w) for w in self._structs)
         self._bound = (hidden, inter, n_expert_used, num_experts, _TORCH_DT[x_dtype], _TORCH_DT[out_dtype],
-                       ACTS[act], workspace.data_ptr(), _nbytes(workspace))
+                       ACTS[act], workspace.data_ptr(), _nbytes(workspace), _PATHS[path])
 
     def __call__(self, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
                  residual: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
@@ -662,11 +672,8 @@ class MoeMlp:
         if residual is not None:
             _want(residual, "MoeMlp: residual", (m, self.hidden), device, (self.out_dtype,))
             r = residual.data_ptr()
-        hidden, inter, S, E, xd, od, act, ws, nbytes = self._bound
-        with _on_device(device):
-            st = self._call(x.data_ptr(), ids.data_ptr(), weights.data_ptr(), self._ptrs[0], self._ptrs[1], r,
-                            out.data_ptr(), m, hidden, inter, S, E, xd, od, act, ws, nbytes, _stream_ptr(device),
-                            _PATHS[self.path])
+        st = _launch(device, self._call, x.data_ptr(), ids.data_ptr(), weights.data_ptr(), *self._ptrs, r,
+                     out.data_ptr(), m, *self._bound)
         if st != MOE_OK:
             raise MoeError(st, "moe_mlp")
         return out

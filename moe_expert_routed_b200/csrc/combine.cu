@@ -4,6 +4,8 @@
 // written once. A thread owns VEC neighbouring columns of one token and walks the
 // slots in order, so the sum (fp32) has one order and no atomics; the residual is
 // added last, before the only rounding.
+#include <string.h>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -38,49 +40,95 @@ template <> struct Cvt<__half> {
 
 template <typename T, int N> struct alignas(sizeof(T) * N) Pack { T v[N]; };
 
-template <typename TZ, typename TO, int VEC>
-__global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(const CombineParams P) {
-    const uint32_t nv = P.n / VEC;
-    for (uint64_t i = (uint64_t)blockIdx.x * COMBINE_THREADS + threadIdx.x; i < P.total;
-         i += (uint64_t)gridDim.x * COMBINE_THREADS) {
-        const uint64_t t = i / nv;
-        const uint32_t c = (uint32_t)(i - t * nv);
-        const Pack<TZ, VEC> *z = (const Pack<TZ, VEC> *)P.z + t * P.S * nv + c;
-        float acc[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; j++) acc[j] = 0.f;
-#pragma unroll 4
-        for (uint32_t s = 0; s < P.S; s++) {
-            if (P.ids && __ldg(P.ids + t * P.S + s) >= P.E) continue;
-            const float w = __ldg(P.w + t * P.S + s);
-            const Pack<TZ, VEC> v = z[(size_t)s * nv];
-#pragma unroll
-            for (int j = 0; j < VEC; j++) acc[j] = fmaf(w, Cvt<TZ>::to(v.v[j]), acc[j]);
-        }
-        Pack<TO, VEC> o;
-        if (P.residual) {
-            const Pack<TO, VEC> r = ((const Pack<TO, VEC> *)P.residual)[i];
-#pragma unroll
-            for (int j = 0; j < VEC; j++) acc[j] += Cvt<TO>::to(r.v[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < VEC; j++) o.v[j] = Cvt<TO>::from(acc[j]);
-        ((Pack<TO, VEC> *)P.out)[i] = o;
+// Read once: not kept in L1.
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> load_once(const Pack<T, N> *p) {
+    Pack<T, N> v;
+    if constexpr (sizeof(v) == 16) {
+        const uint4 u = __ldcs((const uint4 *)p);
+        memcpy(&v, &u, 16);
+    } else if constexpr (sizeof(v) == 8) {
+        const uint2 u = __ldcs((const uint2 *)p);
+        memcpy(&v, &u, 8);
+    } else {
+        v = *p;
     }
+    return v;
+}
+
+// I: 32-bit indices where the sizes allow (the division by nv is several times cheaper).
+// B > 0: the slots are a multiple of B and none is left out, so B rows are requested
+// before the first is used; B = 0: one at a time.
+template <typename TZ, typename TO, int VEC, int B, typename I>
+__global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(const CombineParams P) {
+    const I nv = P.n / VEC;
+    const I i = (I)blockIdx.x * COMBINE_THREADS + threadIdx.x;
+    if (i >= (I)P.total) return;
+    const I t = i / nv;
+    const I c = i - t * nv;
+    const Pack<TZ, VEC> *z = (const Pack<TZ, VEC> *)P.z + (size_t)t * P.S * nv + c;
+    const float *w = P.w + (size_t)t * P.S;
+    float acc[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; j++) acc[j] = 0.f;
+    if constexpr (B > 0) {
+        for (uint32_t s0 = 0; s0 < P.S; s0 += B, z += (size_t)B * nv) {
+            Pack<TZ, VEC> v[B];
+#pragma unroll
+            for (int k = 0; k < B; k++) v[k] = load_once(z + (size_t)k * nv);
+#pragma unroll
+            for (int k = 0; k < B; k++) {
+                const float ws = __ldg(w + s0 + k);
+#pragma unroll
+                for (int j = 0; j < VEC; j++) acc[j] = fmaf(ws, Cvt<TZ>::to(v[k].v[j]), acc[j]);
+            }
+        }
+    } else {
+        for (uint32_t s = 0; s < P.S; s++) {
+            if (P.ids && __ldg(P.ids + (size_t)t * P.S + s) >= P.E) continue;  // not read
+            const float ws = __ldg(w + s);
+            const Pack<TZ, VEC> v = load_once(z + (size_t)s * nv);
+#pragma unroll
+            for (int j = 0; j < VEC; j++) acc[j] = fmaf(ws, Cvt<TZ>::to(v.v[j]), acc[j]);
+        }
+    }
+    Pack<TO, VEC> o;
+    if (P.residual) {
+        const Pack<TO, VEC> r = ((const Pack<TO, VEC> *)P.residual)[i];
+#pragma unroll
+        for (int j = 0; j < VEC; j++) acc[j] += Cvt<TO>::to(r.v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; j++) o.v[j] = Cvt<TO>::from(acc[j]);
+    ((Pack<TO, VEC> *)P.out)[i] = o;
+}
+
+template <typename TZ, typename TO, int VEC, int B>
+cudaError_t launch_b(CombineParams P, uint64_t m, cudaStream_t st) {
+    P.total = m * (P.n / VEC);
+    const uint64_t blocks = (P.total + COMBINE_THREADS - 1) / COMBINE_THREADS;
+    if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
+    if (blocks * COMBINE_THREADS <= 0xFFFFFFFFull)
+        combine_kernel<TZ, TO, VEC, B, uint32_t><<<(uint32_t)blocks, COMBINE_THREADS, 0, st>>>(P);
+    else
+        combine_kernel<TZ, TO, VEC, B, uint64_t><<<(uint32_t)blocks, COMBINE_THREADS, 0, st>>>(P);
+    return cudaGetLastError();
+}
+
+template <typename TZ, typename TO, int VEC>
+cudaError_t launch_v(const CombineParams &P, uint64_t m, cudaStream_t st) {
+    if (P.ids || P.S % 2u) return launch_b<TZ, TO, VEC, 0>(P, m, st);
+    return P.S % 4u ? launch_b<TZ, TO, VEC, 2>(P, m, st) : launch_b<TZ, TO, VEC, 4>(P, m, st);
 }
 
 template <typename TZ, typename TO>
-cudaError_t launch_t(CombineParams P, uint64_t m, cudaStream_t st) {
-    // wide accesses where rows start and end on their boundaries, single elements elsewhere
-    constexpr int W = 4;
+cudaError_t launch_t(const CombineParams &P, uint64_t m, cudaStream_t st) {
+    // 16 bytes of z an access where rows start and end on their boundaries, single elements elsewhere
+    constexpr int W = 16 / sizeof(TZ);
     const uintptr_t za = (uintptr_t)P.z, oa = (uintptr_t)P.out | (uintptr_t)P.residual;
-    const bool wide = P.n % W == 0 && za % (W * sizeof(TZ)) == 0 && oa % (W * sizeof(TO)) == 0;
-    P.total = m * (wide ? P.n / W : P.n);
-    const uint64_t blocks = (P.total + COMBINE_THREADS - 1) / COMBINE_THREADS;
-    const uint32_t grid = (uint32_t)tmin<uint64_t>(blocks, 1u << 20);
-    if (wide) combine_kernel<TZ, TO, W><<<grid, COMBINE_THREADS, 0, st>>>(P);
-    else combine_kernel<TZ, TO, 1><<<grid, COMBINE_THREADS, 0, st>>>(P);
-    return cudaGetLastError();
+    if (P.n % W == 0 && za % (W * sizeof(TZ)) == 0 && oa % (W * sizeof(TO)) == 0)
+        return launch_v<TZ, TO, W>(P, m, st);
+    return launch_v<TZ, TO, 1>(P, m, st);
 }
 
 template <typename TZ>

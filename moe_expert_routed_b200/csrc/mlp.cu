@@ -66,8 +66,8 @@ size_t moe_mlp_workspace_bytes(uint32_t m, uint32_t hidden, uint32_t inter, uint
 moe_status moe_mlp(const void *x, const uint32_t *ids, const float *weights, const moe_expert_weights *gate_up,
                    const moe_expert_weights *down, const void *residual, void *out, uint32_t m, uint32_t hidden,
                    uint32_t inter, uint32_t n_expert_used, uint32_t num_experts, moe_dtype x_dtype,
-                   moe_dtype out_dtype, moe_act act, void *workspace, size_t workspace_bytes, moe_stream_t stream,
-                   moe_path path) {
+                   moe_dtype out_dtype, moe_act act, void *workspace, size_t workspace_bytes, moe_path path,
+                   moe_stream_t stream) {
     if (!m || !hidden || !inter || !n_expert_used || !num_experts || inter > 0x7FFFFFFFu)
         return MOE_ERR_INVALID_ARGUMENT;
     if ((int)x_dtype < 0 || (int)x_dtype > 2 || (int)out_dtype < 0 || (int)out_dtype > 2 || (int)act < 0 ||

@@ -60,8 +60,8 @@ def _mlp(gu=None, dn=None, **kw):
     s1, s2 = struct(gu), struct(dn)
     p1 = None if gu == "null" else ctypes.addressof(s1)
     return M.lib().moe_mlp(a["x"], a["ids"], a["weights"], p1, ctypes.addressof(s2), a["res"], a["out"], a["m"],
-                           a["H"], a["I"], a["S"], a["E"], a["xd"], a["od"], a["act"], a["ws"], a["wsb"], None,
-                           a["path"])
+                           a["H"], a["I"], a["S"], a["E"], a["xd"], a["od"], a["act"], a["ws"], a["wsb"], a["path"],
+                           None)
 
 
 @pytest.mark.parametrize("kw", [dict(m=0), dict(H=0), dict(I=0), dict(S=0), dict(E=0), dict(xd=3), dict(od=-1),
@@ -76,7 +76,7 @@ def test_mlp_refuses_before_cuda(kw):
 
 
 def test_mlp_null_weights_struct():
-    a = M.lib().moe_mlp(16, 16, 16, None, None, None, 16, 4, 128, 64, 2, 8, 1, 1, 0, 4096, 1 << 24, None, 0)
+    a = M.lib().moe_mlp(16, 16, 16, None, None, None, 16, 4, 128, 64, 2, 8, 1, 1, 0, 4096, 1 << 24, 0, None)
     assert a == 1
 
 
