@@ -167,7 +167,7 @@ moe_status run(const void *x, const uint32_t *ids, const void *packed, const voi
                uint32_t bits, moe_fmt fmt, uint32_t n_expert_used, uint32_t num_experts, moe_dtype x_dtype,
                moe_dtype out_dtype, moe_dtype bias_dtype, void *workspace, size_t workspace_bytes,
                moe_stream_t stream, moe_path path, PtrTables pt = {nullptr, nullptr, nullptr}, int act = -1,
-               const W4A4Front *w4 = nullptr) {
+               const W4A4Front *w4 = nullptr, LayerProduct *layer = nullptr) {
     moe_status v = validate(x, ids, pt.packed ? (const void *)pt.packed : packed,
                             pt.packed ? (const void *)pt.scales : scales, aux, out, m, k, n, group_size, bits,
                             fmt, n_expert_used, num_experts, x_dtype, out_dtype);
@@ -270,17 +270,21 @@ moe_status run(const void *x, const uint32_t *ids, const void *packed, const voi
         uint8_t *ximg = nullptr;
         float *tscale = nullptr;
         if (choice == GROUPED && !w4mma && tile_rows == 256u && x_dtype != MOE_F32 && a.kind != K_MXFP4 &&
-            !a.packed_ptrs && a.act < 0 && !a.tok_scale && !a.x_copies && ((uintptr_t)x & 15u) == 0) {
+            !a.packed_ptrs && (a.act < 0 || layer) && !a.tok_scale && !a.x_copies && ((uintptr_t)x & 15u) == 0) {
             const uint64_t ib = x_image_bytes(R, num_experts, k, tile_rows);
             if (workspace_bytes >= L.total + ib + al256(4ull * m)) {
                 ximg = ws + L.total;
                 tscale = (float *)(ws + L.total + ib);
             }
         }
-        ce = launch_route(ids, (uint32_t)R, num_experts, tile_rows, counts, offsets, sp, tiles, tc,
-                          max_tiles, (uint32_t *)(ws + L.chunk_hist),
-                          (uint32_t *)(ws + L.chunk_base), L.chunks, err, out, a.out_n, (int)out_dtype,
-                          st, wc);
+        if (layer && layer->routed == tile_rows)  // the same pairs in the same tiles: only the counter anew
+            ce = cudaMemsetAsync(wc, 0, sizeof(uint32_t), st);
+        else
+            ce = launch_route(ids, (uint32_t)R, num_experts, tile_rows, counts, offsets, sp, tiles, tc,
+                              max_tiles, (uint32_t *)(ws + L.chunk_hist),
+                              (uint32_t *)(ws + L.chunk_base), L.chunks, err, out, a.out_n, (int)out_dtype,
+                              st, wc);
+        if (layer) layer->routed = tile_rows;
         if (ce == cudaSuccess && xg) ce = launch_gather_x(x, (int)x_dtype, sp, (uint32_t)R, k, n_expert_used, xg, st);
         if (ce == cudaSuccess && ximg) {
             ce = launch_x_image(x, (int)x_dtype, m, k, sp, tiles, tc, offsets, n_expert_used, tile_rows, max_tiles,
@@ -302,6 +306,16 @@ moe_status run(const void *x, const uint32_t *ids, const void *packed, const voi
 }
 
 }  // namespace
+
+moe_status run_product(const void *x, const uint32_t *ids, const moe_expert_weights &w, void *out, uint32_t m,
+                       uint32_t k, uint32_t n, uint32_t n_expert_used, uint32_t num_experts, moe_dtype x_dtype,
+                       moe_dtype out_dtype, int act, void *workspace, size_t workspace_bytes, moe_stream_t stream,
+                       moe_path path, LayerProduct *layer) {
+    return run(x, ids, w.packed, w.scales, w.aux, w.bias, out, m, k, n, w.group_size, w.bits, w.fmt, n_expert_used,
+               num_experts, x_dtype, out_dtype, w.bias ? w.bias_dtype : MOE_F32, workspace, workspace_bytes, stream,
+               path, PtrTables{nullptr, nullptr, nullptr}, act, nullptr, layer);
+}
+
 }  // namespace moe
 
 extern "C" {

@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 grouped_gemm_kernel(const GemmParams P, const __grid_constant__ CUtensorMap tmap,
                     const __grid_constant__ CUtensorMap xmap) {
     using C = GemmCfg<KIND, XT, BN>;
-    static_assert(!XIMG || (XT == DT_F16 && !PTRS && !GLU), "the image is f16, for the plain kernel");
+    static_assert(!XIMG || (XT == DT_F16 && !PTRS), "the image is f16, for contiguous weights");
     constexpr int AT = C::AT, BT = C::BT, B_TILE = C::B_TILE;
     constexpr uint32_t STAGE = C::STAGE;
     constexpr bool ATM = C::ATM;
@@ -1043,6 +1043,18 @@ grouped_gemm_kernel(const GemmParams P, const __grid_constant__ CUtensorMap tmap
             if (!next_item(i, true, w) || w >= n_items) break;
             if (!load_item(w)) continue;
             const uint32_t buf = done % NACC, use = done / NACC;
+            const uint32_t *pairs = P.sorted_pairs + it.off + it.r0;
+            // lane j < 16 fetches column c0 + j's pair and its token's factor, a chunk ahead of
+            // their use and the first before the accumulator is ready: two dependent loads
+            // from L2 a chunk would otherwise outlast the mainloop of a short k
+            auto fetch = [&](uint32_t c0, uint32_t &p, float &f) {
+                const uint32_t cj = c0 + (lane & 15u);
+                p = cj < it.nt ? __ldg(pairs + cj) : 0u;
+                f = P.tok_scale ? __ldg(P.tok_scale + p / P.n_expert_used) : 1.f;
+            };
+            uint32_t nextp;
+            float nextf;
+            fetch(0u, nextp, nextf);
             if (!ptx::mbar_wait_bounded(accfull0 + 8 * buf, use & 1u, abort_flag, P.err, ERR_TIMEOUT, P.timeout_ns))
                 break;
             ptx::tc_fence_after();
@@ -1052,15 +1064,12 @@ grouped_gemm_kernel(const GemmParams P, const __grid_constant__ CUtensorMap tmap
             const float s2 = (KIND == K_NVFP4) ? __ldg((const float *)P.aux + it.e) : 1.f;
             const float bv =
                 grow_e < P.n ? load_bias(P.bias, P.bias_dtype, (size_t)it.e * P.n + glu_row(grow_e, nh)) : 0.f;
-            const uint32_t *pairs = P.sorted_pairs + it.off + it.r0;
             for (uint32_t c0 = 0; c0 < it.nt; c0 += 16) {
                 uint32_t v[16], pr[16];
                 ptx::tmem_ld16(d + ((q * 32u) << 16) + c0, v);
-                // lane j < 16 fetches column c0 + j's pair (and its token's factor); the
-                // warp shares them by shuffles
-                const uint32_t cj = c0 + (lane & 15u);
-                const uint32_t myp = cj < it.nt ? __ldg(pairs + cj) : 0u;
-                const float myf = P.tok_scale ? __ldg(P.tok_scale + myp / P.n_expert_used) : 1.f;
+                const uint32_t myp = nextp;
+                const float myf = nextf;
+                if (c0 + 16u < it.nt) fetch(c0 + 16u, nextp, nextf);
 #pragma unroll
                 for (int i = 0; i < 16; i++) pr[i] = __shfl_sync(0xFFFFFFFFu, myp, i);
                 ptx::tmem_wait_ld();
@@ -1072,14 +1081,17 @@ grouped_gemm_kernel(const GemmParams P, const __grid_constant__ CUtensorMap tmap
                         v[i] = __float_as_uint(__uint_as_float(v[i]) * __shfl_sync(0xFFFFFFFFu, myf, i));
                 }
                 if constexpr (GLU) {
-                    // even lanes hold gate rows, the next lane the matching up row
+                    // even lanes hold gate rows, the next lane the matching up row: of two
+                    // columns the even lane takes the first, the odd lane the second
+                    const bool odd = lane & 1u;
 #pragma unroll
-                    for (int i = 0; i < 16; i++) {
-                        const float y = __uint_as_float(v[i]) * s2 + bv;
-                        const float up = __shfl_xor_sync(0xFFFFFFFFu, y, 1);
-                        const uint32_t col = c0 + i;
-                        if (col < it.nt && grow_e < P.n && !(lane & 1u))
-                            store_out(P.out, P.out_dtype, (size_t)pr[i] * nh + (grow_e >> 1), glu_act(P.act, y) * up);
+                    for (int i = 0; i < 16; i += 2) {
+                        const float y0 = __uint_as_float(v[i]) * s2 + bv, y1 = __uint_as_float(v[i + 1]) * s2 + bv;
+                        const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? y0 : y1, 1);
+                        const float gate = odd ? other : y0, up = odd ? y1 : other;
+                        if (c0 + i + (odd ? 1u : 0u) < it.nt && grow_e < P.n)
+                            store_out(P.out, P.out_dtype, (size_t)(odd ? pr[i + 1] : pr[i]) * nh + (grow_e >> 1),
+                                      glu_act(P.act, gate) * up);
                     }
                 } else if (grow_e < P.n) {
                     const uint32_t nc = tmin<uint32_t>(16u, it.nt - c0);
@@ -1195,6 +1207,10 @@ template <int KIND, int XT, int BN>
 cudaError_t launch_t(const GemmParams &P, const CUtensorMap &tm, const CUtensorMap &xm, const GemmPlan &pl,
                      uint32_t n_mtiles, uint32_t max_tiles, cudaStream_t st) {
     if (P.packed_ptrs) return launch_tp<KIND, XT, BN, true, false>(P, tm, xm, pl, n_mtiles, max_tiles, st);
+    if constexpr (XT == DT_F16 && BN == 256) {  // the image has 256-pair tiles
+        if (P.glu_nh && P.xmode == XM_IMAGE)
+            return launch_tp<KIND, XT, BN, false, true, true>(P, tm, xm, pl, n_mtiles, max_tiles, st);
+    }
     if (P.glu_nh) return launch_tp<KIND, XT, BN, false, true>(P, tm, xm, pl, n_mtiles, max_tiles, st);
     if constexpr (XT == DT_F16) {
         if (P.xmode == XM_IMAGE) return launch_tp<KIND, XT, BN, false, false, true>(P, tm, xm, pl, n_mtiles, max_tiles, st);
@@ -1383,7 +1399,7 @@ cudaError_t launch_gemm(const QmmArgs &a, const uint32_t *offsets, const uint32_
                   : XM_LOADERS;
     // 16-bit x as the f16 image (the caller sets a.x_dtype to f16 with it)
     P.ximage = nullptr;
-    if (ximg && a.x_dtype == DT_F16 && !a.packed_ptrs && a.act < 0) {
+    if (ximg && a.x_dtype == DT_F16 && !a.packed_ptrs) {
         P.xmode = XM_IMAGE;
         P.ximage = ximg;
     }

@@ -132,6 +132,19 @@ cudaError_t launch_combine(const void *z, const float *weights, const uint32_t *
                            uint32_t m, uint32_t S, uint32_t n, uint32_t E, int z_dtype, int out_dtype,
                            cudaStream_t st);
 
+// A product inside moe_mlp: what moe_qmm_id_glu / _bias / _path run, and what the layer's
+// two products share. With `layer` set, a gated output of 256-pair tiles takes the f16
+// image of x where the workspace has room, the routing left in the workspace by the
+// product before it (tiles of `routed` rows; 0: none) is taken over, and rows of pairs
+// with an id out of range are then not written.
+struct LayerProduct {
+    uint32_t routed;
+};
+moe_status run_product(const void *x, const uint32_t *ids, const moe_expert_weights &w, void *out, uint32_t m,
+                       uint32_t k, uint32_t n, uint32_t n_expert_used, uint32_t num_experts, moe_dtype x_dtype,
+                       moe_dtype out_dtype, int act, void *workspace, size_t workspace_bytes, moe_stream_t stream,
+                       moe_path path, LayerProduct *layer);
+
 // moe_mlp's checked arguments.
 struct MlpArgs {
     const void *x;

@@ -93,18 +93,14 @@ moe_status moe_mlp(const void *x, const uint32_t *ids, const float *weights, con
     if (path != MOE_PATH_GROUPED && mlp_few_supported(a))
         return launch_mlp_few(a, (uint32_t *)ws, h, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     const moe_dtype hd = h_dtype((int)x_dtype);
-    v = moe_qmm_id_glu(x, ids, gate_up->packed, gate_up->scales, gate_up->aux, gate_up->bias, h, m, hidden,
-                       2u * inter, gate_up->group_size, gate_up->bits, gate_up->fmt, n_expert_used, num_experts,
-                       x_dtype, hd, gate_up->bias_dtype, act, workspace, L.own, stream, path);
+    LayerProduct layer{0u};
+    v = run_product(x, ids, *gate_up, h, m, hidden, 2u * inter, n_expert_used, num_experts, x_dtype, hd, (int)act,
+                    workspace, L.own, stream, path, &layer);
     if (v != MOE_OK) return v;
-    // every (token, slot) pair is a token of its own here, with its own row of h
-    if (down->bias)
-        v = moe_qmm_id_bias(h, ids, down->packed, down->scales, down->aux, down->bias, z, R, inter, hidden,
-                            down->group_size, down->bits, down->fmt, 1, num_experts, hd, MOE_F32, down->bias_dtype,
-                            workspace, L.own, stream, path);
-    else
-        v = moe_qmm_id_path(h, ids, down->packed, down->scales, down->aux, z, R, inter, hidden, down->group_size,
-                            down->bits, down->fmt, 1, num_experts, hd, MOE_F32, workspace, L.own, stream, path);
+    // every (token, slot) pair is a token of its own here, with its own row of h; pairs
+    // left out have no row of z
+    v = run_product(h, ids, *down, z, R, inter, hidden, 1, num_experts, hd, MOE_F32, -1, workspace, L.own, stream, path,
+                    &layer);
     if (v != MOE_OK) return v;
     return launch_combine(z, weights, ids, residual, out, m, n_expert_used, hidden, num_experts, DT_F32,
                           (int)out_dtype, (cudaStream_t)stream) == cudaSuccess

@@ -245,18 +245,22 @@ gather_x(const float *__restrict__ x, const uint32_t *__restrict__ sorted_pairs,
 // unless it falls below f16's normal range (2^-14, i.e. below 2^-28 of the token's
 // largest). tok_scale[t] = 2^(E-15) undoes it in the GEMM's epilogue (1 for a zero row).
 __global__ void __launch_bounds__(256)
-x_token_scale(const uint16_t *__restrict__ x, uint32_t k, float *__restrict__ tok_scale) {
-    __shared__ float red[8];
-    const uint32_t t = blockIdx.x;
-    float a = 0.f;
-    for (uint32_t j = threadIdx.x; j < k; j += 256u) a = fmaxf(a, fabsf(bf16_bits_to_f32(__ldg(x + (size_t)t * k + j))));
+x_token_scale(const uint16_t *__restrict__ x, uint32_t m, uint32_t k, float *__restrict__ tok_scale) {
+    // one warp a token, 16 bytes a lane (rows are multiples of 16 bytes)
+    const uint32_t t = blockIdx.x * 8u + (threadIdx.x >> 5), lane = threadIdx.x & 31u;
+    if (t >= m) return;
+    const uint4 *row = (const uint4 *)(x + (size_t)t * k);
+    uint32_t a = 0;  // |bf16| bits order like the values
+#pragma unroll 4
+    for (uint32_t j = lane; j < k / 8u; j += 32u) {
+        const uint4 v = __ldg(row + j);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, d));
-    if ((threadIdx.x & 31u) == 0) red[threadIdx.x >> 5] = a;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < 8; w++) a = fmaxf(a, red[w]);
-        const int e = a > 0.f ? ((int)((__float_as_uint(a) >> 23) & 0xFFu) - 126) : 15;  // a < 2^e
+        for (int i = 0; i < 4; i++) a = __vmaxu2(a, w[i] & 0x7FFF7FFFu);
+    }
+    a = __reduce_max_sync(0xFFFFFFFFu, max(a & 0xFFFFu, a >> 16));
+    if (lane == 0) {
+        const int e = a ? ((int)(a >> 7) - 126) : 15;  // |x| < 2^e
         const int s = e - 15 < -126 ? -126 : (e - 15 > 127 ? 127 : e - 15);
         tok_scale[t] = __uint_as_float((uint32_t)(s + 127) << 23);
     }
@@ -336,7 +340,7 @@ cudaError_t launch_x_image(const void *x, int x_dtype, uint32_t m, uint32_t k, c
     const uint16_t *x16 = (const uint16_t *)x;
     if (x_dtype == DT_BF16) {
         if (!tok_scale) return cudaErrorInvalidValue;
-        x_token_scale<<<m, 256, 0, st>>>(x16, k, tok_scale);
+        x_token_scale<<<(m + 7u) / 8u, 256, 0, st>>>(x16, m, k, tok_scale);
     } else {
         tok_scale = nullptr;
     }
