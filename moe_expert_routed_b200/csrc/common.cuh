@@ -37,6 +37,8 @@ __host__ __device__ constexpr int kind_bits(int kind) {
 
 template <typename T>
 __host__ __device__ __forceinline__ T tmin(T a, T b) { return a < b ? a : b; }
+template <typename T>
+__host__ __device__ __forceinline__ T tmax(T a, T b) { return a > b ? a : b; }
 
 // --------------------------------------------------------------- decoders
 

@@ -45,6 +45,8 @@ constexpr uint32_t RING = 3;             // steps of a warp in flight
 constexpr uint32_t UP_TILES = 2;         // mlp_up: tiles of 16 rows a warp works on at once
 constexpr uint32_t UP_PARTS = 4;         // mlp_up: warps that share a pair of tiles, each a part of hidden
 constexpr uint32_t MAX_SPLIT = 4;        // mlp_down: CTAs that share 16 columns
+constexpr uint32_t FEW_ALONE_R = 16;     // pairs up to which mlp_down's CTAs share no columns
+constexpr uint32_t SMS = 148;
 constexpr size_t FEW_SMEM = 216 * 1024;
 
 // Storage as the kernels are specialised for it: affine with groups of two units or more
@@ -886,7 +888,7 @@ cudaError_t up_t(const FewParams &P, cudaStream_t st) {
     // about two waves of two CTAs an SM if every pair has an expert of its own: further
     // units of an expert follow in the same CTA, which saves it the prologue
     const uint32_t experts = tmin<uint32_t>(P.R, P.E);
-    const uint32_t gx = tmin<uint32_t>((4u * 148u + experts - 1u) / experts, P.I / 32u);
+    const uint32_t gx = tmin<uint32_t>((4u * SMS + experts - 1u) / experts, P.I / 32u);
     kern<<<dim3(gx, P.R), FEW_THREADS, smem, st>>>(P);
     return cudaGetLastError();
 }
@@ -937,9 +939,9 @@ cudaError_t up_p(const FewParams &P, cudaStream_t st) {
 
 template <int MODE, int NPL>
 cudaError_t down_p(const FewParams &P, cudaStream_t st) {
-    // a single token's columns on as many SMs as there are; else two tiles a warp, which
+    // a token's columns on as many SMs as there are; else two tiles a warp, which
     // share a step's B registers and its loop
-    if (P.split == 1u) return down_t<MODE, NPL, 1, 1>(P, st);
+    if (P.R <= FEW_ALONE_R) return down_t<MODE, NPL, 1, 1>(P, st);
     uint32_t blocks = blocks_a_pass(P, NPL);
     while (blocks > 1u && down_bytes(affine(MODE), P.I, P.g2, NPL, blocks, 2, P.m) > FEW_SMEM) blocks /= 2u;
     switch (blocks) {
@@ -1024,9 +1026,10 @@ cudaError_t launch_mlp_few(const MlpArgs &a, uint32_t *err, void *hf, cudaStream
     const int m1 = mode_of(*a.gate_up, a.hidden), m2 = mode_of(*a.down, a.inter);
     P.scale2_kind = m2 == M_NV;
     P.down_affine = affine(m2);
-    // CTAs enough for even shares of the SMs, where the work outweighs the join
-    P.split = 1u;
-    if (P.R > 16u) P.split = P.H / 32u * 2u >= 5u * 148u / 2u ? 2u : MAX_SPLIT;
+    // mlp_down's CTAs: up to one wave of two an SM (a second wave would pay its prologue
+    // again: 58 us against 62 with 3 and 4 CTAs a block of 88, 61 against 64 with 2 and 4
+    // of 128); a token or two have too little work to be worth the join
+    P.split = P.R <= FEW_ALONE_R ? 1u : tmin<uint32_t>(tmax<uint32_t>(2u * SMS / (P.H / 32u), 1u), MAX_SPLIT);
     const cudaError_t ce = m1 == M_AFF    ? up_m<M_AFF>(P, st)
                            : m1 == M_AFF1 ? up_m<M_AFF1>(P, st)
                            : m1 == M_NV   ? up_m<M_NV>(P, st)
