@@ -3,12 +3,14 @@
 //
 // One warp per token. Lane l holds logits l, l + 32, ... in registers as keys
 // whose unsigned order is the order of the choice; each of the k rounds takes the
-// largest key of the warp (redux.max), the lowest expert that has it (redux.min),
-// and retires it in the lane that holds it. Softmax and sigmoid are monotonic, so
-// without a selection bias the choice is made on the logits themselves and is
-// exact. With a bias the choice is by sigmoid(l) + b: two experts can then lie
-// closer than a 32-bit sigmoid tells apart, so that sum is formed in 64 bits and
-// compared as a 64-bit key (two redux rounds).
+// largest key of the warp (redux.max) and the lowest expert that has it (redux.min),
+// and retires it where it is. Bound by the ALU: about five instructions a round for
+// each register, so the registers are as few as the experts need. (Looking for the
+// key by a vote and a branch a register took more, and longer for few tokens.)
+// Softmax and sigmoid are monotonic, so without a selection bias the choice is made
+// on the logits themselves and is exact. With a bias the choice is by sigmoid(l) + b:
+// two experts can then lie closer than a 32-bit sigmoid tells apart, so that sum is
+// formed in 64 bits and compared as a 64-bit key (two redux rounds).
 #include "common.cuh"
 #include "internal.h"
 
@@ -30,8 +32,6 @@ __device__ __forceinline__ uint64_t key64(double v) {
     const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
     return (u >> 63) ? ~u : u | (1ull << 63);
 }
-
-__device__ __forceinline__ float load_logit(const void *p, int dt, size_t i) { return load_x(p, dt, i); }
 
 struct GateParams {
     const void *logits;
@@ -55,27 +55,23 @@ __global__ void __launch_bounds__(GATE_WARPS * 32) gate_topk(const GateParams P)
 #pragma unroll
     for (int j = 0; j < V; j++) {
         const uint32_t e = j * 32u + lane;
-        l[j] = e < P.E ? load_logit(P.logits, P.dtype, row + e) : 0.f;
+        l[j] = e < P.E ? load_x(P.logits, P.dtype, row + e) : 0.f;
     }
-    bool nan = false;
 #pragma unroll
     for (int j = 0; j < V; j++) {
         const uint32_t e = j * 32u + lane;
-        const bool in = e < P.E;
         if constexpr (BIAS) {
             const uint64_t key =
-                in ? key64(1.0 / (1.0 + exp(-(double)l[j])) + (double)__ldg(P.bias + e)) : 0ull;
+                e < P.E ? key64(1.0 / (1.0 + exp(-(double)l[j])) + (double)__ldg(P.bias + e)) : 0ull;
             hi[j] = (uint32_t)(key >> 32);
             lo[j] = (uint32_t)key;
         } else {
-            hi[j] = in ? key32(l[j]) : 0u;
+            hi[j] = e < P.E ? key32(l[j]) : 0u;
         }
-        nan |= in && l[j] != l[j];
     }
 
-    // rounds: lane r keeps the r-th choice (k <= 32)
+    // rounds: lane r keeps the r-th choice (k <= 32 and k <= E: a key above 0 is left)
     uint32_t my_e = 0;
-    float my_l = 0.f;
     for (uint32_t r = 0; r < P.k; r++) {
         uint32_t top = 0, low = 0;
         if constexpr (BIAS) {
@@ -90,28 +86,27 @@ __global__ void __launch_bounds__(GATE_WARPS * 32) gate_topk(const GateParams P)
             for (int j = 0; j < V; j++) top = max(top, hi[j]);
             top = __reduce_max_sync(FULL, top);
         }
-        uint32_t e = FULL;
+        uint32_t slot = FULL;  // the lowest register of this lane that has it
 #pragma unroll
         for (int j = V - 1; j >= 0; j--) {
-            bool is = hi[j] == top && j * 32u + lane < P.E;
+            bool is = hi[j] == top;
             if constexpr (BIAS) is = is && lo[j] == low;
-            if (is) e = j * 32u + lane;
+            if (is) slot = j;
         }
-        e = __reduce_min_sync(FULL, e);
-        float v = 0.f;
+        const uint32_t e = __reduce_min_sync(FULL, slot == FULL ? FULL : slot * 32u + lane);
+        if ((e & 31u) != lane) slot = FULL;
 #pragma unroll
         for (int j = 0; j < V; j++)
-            if (j * 32u + lane == e) {
-                v = l[j];
+            if (slot == (uint32_t)j) {
                 hi[j] = 0u;
                 if constexpr (BIAS) lo[j] = 0u;
             }
-        v = __shfl_sync(FULL, v, e & 31u);
-        if (lane == r) my_e = e, my_l = v;
+        if (lane == r) my_e = e;
     }
 
     // weights of the chosen
     const bool mine = lane < P.k;
+    const float my_l = mine ? load_x(P.logits, P.dtype, row + my_e) : 0.f;
     float p = 0.f, den = 1.f;
     if (P.sigmoid) {
         // in 64 bits: far below zero a 32-bit sigmoid leaves nothing to renormalise
@@ -124,13 +119,7 @@ __global__ void __launch_bounds__(GATE_WARPS * 32) gate_topk(const GateParams P)
         }
         p = (float)s;
     } else {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < V; j++)
-            if (j * 32u + lane < P.E) mx = fmaxf(mx, l[j]);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, d));
-        const bool none = mx == -INFINITY && !__any_sync(FULL, nan);  // every expert masked
+        const float mx = __shfl_sync(FULL, my_l, 0);  // the first choice
         p = mine ? expf(my_l - mx) : 0.f;
         float sum = p;
         if (!P.renorm) {
@@ -142,7 +131,12 @@ __global__ void __launch_bounds__(GATE_WARPS * 32) gate_topk(const GateParams P)
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(FULL, sum, d);
         den = sum;
-        if (none) p = 0.f, den = 1.f;
+        if (mx == -INFINITY) {  // every expert masked: weights 0, unless a NaN is among them
+            bool nan = false;
+#pragma unroll
+            for (int j = 0; j < V; j++) nan |= l[j] != l[j];
+            if (!__any_sync(FULL, nan)) p = 0.f, den = 1.f;
+        }
     }
     if (mine) {
         const size_t o = t * P.k + lane;
@@ -154,12 +148,20 @@ __global__ void __launch_bounds__(GATE_WARPS * 32) gate_topk(const GateParams P)
 template <bool BIAS>
 cudaError_t launch_v(const GateParams &P, cudaStream_t st) {
     const dim3 grid((P.m + GATE_WARPS - 1) / GATE_WARPS), block(GATE_WARPS * 32);
-    if (P.E <= 32) gate_topk<1, BIAS><<<grid, block, 0, st>>>(P);
-    else if (P.E <= 64) gate_topk<2, BIAS><<<grid, block, 0, st>>>(P);
-    else if (P.E <= 128) gate_topk<4, BIAS><<<grid, block, 0, st>>>(P);
-    else if (P.E <= 256) gate_topk<8, BIAS><<<grid, block, 0, st>>>(P);
-    else if (P.E <= 512) gate_topk<16, BIAS><<<grid, block, 0, st>>>(P);
-    else gate_topk<32, BIAS><<<grid, block, 0, st>>>(P);
+    switch ((P.E + 31u) / 32u) {
+        case 1: gate_topk<1, BIAS><<<grid, block, 0, st>>>(P); break;
+        case 2: gate_topk<2, BIAS><<<grid, block, 0, st>>>(P); break;
+        case 3: gate_topk<3, BIAS><<<grid, block, 0, st>>>(P); break;
+        case 4: gate_topk<4, BIAS><<<grid, block, 0, st>>>(P); break;
+        case 5: gate_topk<5, BIAS><<<grid, block, 0, st>>>(P); break;
+        case 6: gate_topk<6, BIAS><<<grid, block, 0, st>>>(P); break;
+        case 7:
+        case 8: gate_topk<8, BIAS><<<grid, block, 0, st>>>(P); break;
+        default:
+            if (P.E <= 384) gate_topk<12, BIAS><<<grid, block, 0, st>>>(P);
+            else if (P.E <= 512) gate_topk<16, BIAS><<<grid, block, 0, st>>>(P);
+            else gate_topk<32, BIAS><<<grid, block, 0, st>>>(P);
+    }
     return cudaGetLastError();
 }
 
