@@ -49,11 +49,19 @@ constexpr uint32_t FEW_ALONE_R = 16;     // pairs up to which mlp_down's CTAs sh
 constexpr uint32_t SMS = 148;
 constexpr size_t FEW_SMEM = 216 * 1024;
 
-// Storage as the kernels are specialised for it: affine with groups of two units or more
-// (one scale for the two units of a lane's accumulator columns), affine with groups of
-// one unit, NVFP4 (two scales a unit), MXFP4.
-enum Mode : int { M_AFF, M_AFF1, M_NV, M_MX };
-constexpr bool affine(int mode) { return mode == M_AFF || mode == M_AFF1; }
+// Storage as the kernels are specialised for it: affine 4 bits with groups of two units or
+// more (one scale for the two units of a lane's accumulator columns) or of one unit,
+// affine 6 and 8 bits, NVFP4 (two scales a unit), MXFP4, codebooks of 2, 3 and 4 bits.
+enum Mode : int { M_A4, M_A4U, M_A6, M_A8, M_NV, M_MX, M_CB2, M_CB3, M_CB4 };
+__host__ __device__ constexpr bool affine(int m) { return m == M_A4 || m == M_A4U || m == M_A6 || m == M_A8; }
+__host__ __device__ constexpr bool codebook(int m) { return m == M_CB2 || m == M_CB3 || m == M_CB4; }
+
+// A lane's unit of 32 codes of one row, as it is copied: pieces of 4, 8 or 16 bytes.
+__host__ __device__ constexpr uint32_t piece(int m) { return m == M_CB3 ? 4u : m == M_A6 || m == M_CB2 ? 8u : 16u; }
+__host__ __device__ constexpr uint32_t pieces(int m) { return m == M_CB3 ? 4u : m == M_A6 ? 3u : m == M_A8 ? 2u : 1u; }
+constexpr int words(int m) { return (int)(piece(m) * pieces(m) / 4u); }
+// The units of 8 rows in the ring: [piece][lane].
+__host__ __device__ constexpr uint32_t rows8(int m) { return 32u * piece(m) * pieces(m); }
 
 // Planes of x by its type, of h by the result's.
 constexpr int x_planes(int dt) { return dt == DT_F32 ? 2 : 1; }
@@ -66,6 +74,16 @@ __host__ __device__ constexpr uint32_t step_bytes(int planes) { return (uint32_t
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
 }
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {
@@ -81,31 +99,162 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
 
 // --------------------------------------------------------------------- codes
 
-// Eight 4-bit codes of a word as f16 pairs: affine (0, 4), (1, 5), (2, 6), (3, 7) times
-// 2^-24, the second and fourth pair 16 times that; E2M1 (0, 1), (2, 3), (4, 5), (6, 7).
-template <bool AFFINE>
-__device__ __forceinline__ void expand(uint32_t w, uint32_t (&p)[4]) {
-    if constexpr (AFFINE) {
-        p[0] = w & 0x000F000Fu;
-        p[1] = w & 0x00F000F0u;
-        p[2] = (w >> 8) & 0x000F000Fu;
-        p[3] = (w >> 8) & 0x00F000F0u;
-    } else {
+// Byte of a row at which unit u's pieces begin (3-bit words hold 10 codes: its first word).
+template <int MODE>
+__device__ __forceinline__ uint32_t unit_byte(uint32_t u) {
+    if constexpr (MODE == M_CB3) return (32u * u / 10u) * 4u;
+    else return u * piece(MODE) * pieces(MODE);
+}
+
+// Copies one unit (zeros where `in` is 0: nothing is read then).
+template <int MODE>
+__device__ __forceinline__ void copy_unit(uint32_t dst, const uint8_t *src, uint32_t in) {
+#pragma unroll
+    for (uint32_t k = 0; k < pieces(MODE); k++) {
+        const uint32_t d = dst + k * 32u * piece(MODE);
+        const uint8_t *s = src + k * piece(MODE);
+        if constexpr (piece(MODE) == 16u) ptx::cp_async_16(d, s, in ? 16u : 0u);
+        else if constexpr (piece(MODE) == 8u) ptx::cp_async_8(d, s, in ? 8u : 0u);
+        else ptx::cp_async_4(d, s, in ? 4u : 0u);
+    }
+}
+
+template <int MODE>
+__device__ __forceinline__ void load_unit(uint32_t a, uint32_t (&w)[words(MODE)]) {
+#pragma unroll
+    for (uint32_t k = 0; k < pieces(MODE); k++) {
+        const uint32_t at = a + k * 32u * piece(MODE);
+        if constexpr (piece(MODE) == 16u) {
+            const uint4 v = lds128(at);
+            w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
+        } else if constexpr (piece(MODE) == 8u) {
+            const uint2 v = lds64(at);
+            w[2 * k] = v.x; w[2 * k + 1] = v.y;
+        } else {
+            w[k] = lds32(at);
+        }
+    }
+}
+
+// Byte permutation as the instruction does it: bit 3 of a selector repeats the byte's sign
+// (__byte_perm drops it, with an instruction of its own).
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+    return d;
+}
+
+// The f16 codebook's low and high bytes, as the byte permutation looks them up.
+template <int MODE>
+struct Table {
+    static constexpr int N = MODE == M_CB4 ? 4 : MODE == M_CB3 ? 2 : 1;
+    uint32_t lo[N], hi[N];
+    __device__ __forceinline__ void load(const uint8_t *cb) {
+        if constexpr (codebook(MODE)) {
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                lo[i] = hi[i] = 0u;
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const uint32_t v = __ldg((const unsigned short *)cb + 4 * i + k);
+                    lo[i] |= (v & 0xFFu) << (8 * k);
+                    hi[i] |= (v >> 8) << (8 * k);
+                }
+            }
+        }
+    }
+    // Four codes, one in each nibble of the low half of `sel`, as two f16 pairs.
+    __device__ __forceinline__ void look(uint32_t sel, uint32_t &p, uint32_t &q) const {
+        uint32_t l, h;
+        if constexpr (N < 4) {
+            l = prmt(lo[0], lo[N - 1], sel);
+            h = prmt(hi[0], hi[N - 1], sel);
+        } else {
+            const uint32_t s7 = sel & 0x7777u, s8 = sel & 0x8888u;
+            const uint32_t upper = prmt(0x00008000u, 0u, s8 | (s8 >> 3));  // 0xFF where the code is 8 or more
+            l = (prmt(lo[0], lo[1], s7) & ~upper) | (prmt(lo[2], lo[3], s7) & upper);
+            h = (prmt(hi[0], hi[1], s7) & ~upper) | (prmt(hi[2], hi[3], s7) & upper);
+        }
+        p = prmt(l, h, 0x5140);
+        q = prmt(l, h, 0x7362);
+    }
+};
+
+// A unit's words before they are expanded: 3-bit words of 10 codes joined into 96 bits
+// from the unit's first code on (word_codes = codes before it in its first word).
+template <int MODE>
+__device__ __forceinline__ void join_words(uint32_t (&w)[words(MODE)], uint32_t word_codes) {
+    if constexpr (MODE == M_CB3) {
+        const uint32_t m = 0x3FFFFFFFu, a = w[0] & m, b = w[1] & m, c = w[2] & m, d = w[3] & m;
+        const uint32_t x0 = a | (b << 30), x1 = (b >> 2) | (c << 28), x2 = (c >> 4) | (d << 26), x3 = d >> 6;
+        const uint32_t s = 3u * word_codes;
+        w[0] = __funnelshift_r(x0, x1, s);
+        w[1] = __funnelshift_r(x1, x2, s);
+        w[2] = __funnelshift_r(x2, x3, s);
+    }
+}
+
+// Codes 8 t .. 8 t + 7 of a unit as f16 pairs:
+//   affine, as integers times 2^-24: 4 bits (0, 4), (1, 5), (2, 6), (3, 7), the second and
+//   fourth pair 16 times that; 8 bits (0, 2), (1, 3), (4, 6), (5, 7); 6 bits in order
+//   E2M1 and codebook values in order: (0, 1), (2, 3), (4, 5), (6, 7)
+template <int MODE>
+__device__ __forceinline__ void expand(const uint32_t (&w)[words(MODE)], int t, const Table<MODE> &T, uint32_t (&p)[4]) {
+    if constexpr (MODE == M_A4 || MODE == M_A4U) {
+        p[0] = w[t] & 0x000F000Fu;
+        p[1] = w[t] & 0x00F000F0u;
+        p[2] = (w[t] >> 8) & 0x000F000Fu;
+        p[3] = (w[t] >> 8) & 0x00F000F0u;
+    } else if constexpr (MODE == M_A8) {
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            p[2 * i] = w[2 * t + i] & 0x00FF00FFu;
+            p[2 * i + 1] = (w[2 * t + i] >> 8) & 0x00FF00FFu;
+        }
+    } else if constexpr (MODE == M_A6) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int bit = 48 * t + 12 * i, k = bit / 32, s = bit % 32;
+            const uint32_t v = s <= 20 ? w[k] >> s : __funnelshift_r(w[k], w[k + 1 < 6 ? k + 1 : k], s);
+            p[i] = (v & 0x3Fu) | ((v << 10) & 0x003F0000u);
+        }
+    } else if constexpr (MODE == M_NV || MODE == M_MX) {
         asm("{.reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %4; cvt.rn.f16x2.e2m1x2 %0, a; cvt.rn.f16x2.e2m1x2 %1, b; "
             "cvt.rn.f16x2.e2m1x2 %2, c; cvt.rn.f16x2.e2m1x2 %3, d;}"
             : "=r"(p[0]), "=r"(p[1]), "=r"(p[2]), "=r"(p[3])
-            : "r"(w));
+            : "r"(w[t]));
+    } else {
+        // the codes spread to nibbles: halves, quarters and eighths apart
+        uint32_t n;
+        if constexpr (MODE == M_CB4) {
+            n = w[t];
+        } else if constexpr (MODE == M_CB2) {
+            const uint32_t v = t & 1 ? w[t / 2] >> 16 : w[t / 2];
+            n = (v & 0xFFu) | ((v << 8) & 0x00FF0000u);
+            n = (n & 0x000F000Fu) | ((n << 4) & 0x0F000F00u);
+            n = (n & 0x03030303u) | ((n << 2) & 0x30303030u);
+        } else {
+            const uint32_t v = t == 0 ? w[0] : t == 1 ? __funnelshift_r(w[0], w[1], 24)
+                             : t == 2 ? __funnelshift_r(w[1], w[2], 16) : w[2] >> 8;
+            n = (v & 0xFFFu) | ((v << 4) & 0x0FFF0000u);
+            n = (n & 0x003F003Fu) | ((n << 2) & 0x3F003F00u);
+            n = (n & 0x07070707u) | ((n << 1) & 0x70707070u);
+        }
+        T.look(n, p[0], p[1]);
+        T.look(n >> 16, p[2], p[3]);
     }
 }
 // What expand()'s values have to be multiplied by.
 constexpr float code_unit(int mode) { return affine(mode) ? 16777216.f : 1.f; }
 
-// Place of value c of a unit among its 32 f16 values, as expand() pairs the codes, and
-// whether it meets a code of the 16-fold pairs.
-__device__ __forceinline__ uint32_t b_place(bool aff, uint32_t c) {
-    return aff ? (c & ~7u) + 2u * (c & 3u) + ((c >> 2) & 1u) : c;
+// Order of x against expand()'s pairs: 0 as it stands, 1 as 4-bit affine words part it
+// (with a sixteenth of the values that meet the 16-fold pairs), 2 as 8-bit words do.
+constexpr int order_of(int mode) { return mode == M_A4 || mode == M_A4U ? 1 : mode == M_A8 ? 2 : 0; }
+// Place of value c of a unit among its 32 f16 values.
+__device__ __forceinline__ uint32_t b_place(int order, uint32_t c) {
+    return order == 1 ? (c & ~7u) + 2u * (c & 3u) + ((c >> 2) & 1u)
+         : order == 2 ? (c & ~3u) + 2u * (c & 1u) + ((c >> 1) & 1u) : c;
 }
-__device__ __forceinline__ bool b_sixteenth(bool aff, uint32_t c) { return aff && (c & 1u); }
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -143,7 +292,9 @@ __device__ __forceinline__ void unit_scale(uint32_t maxbits, float &scale, float
 }
 
 // Bytes of one row's scales.
-__host__ __device__ constexpr uint32_t scale_bytes(bool aff, uint32_t groups) { return aff ? groups * 2u : groups; }
+__host__ __device__ constexpr uint32_t scale_bytes(int mode, uint32_t groups) {
+    return affine(mode) || codebook(mode) ? groups * 2u : groups;
+}
 
 // ------------------------------------------------------------------ one step
 
@@ -177,7 +328,7 @@ __device__ __forceinline__ StepAt<NB> step_at(uint32_t base, uint32_t stride, ui
 // its accumulator columns; NVFP4 units have two.
 template <int MODE>
 struct Scales {
-    static constexpr int PARTS = MODE == M_NV ? 2 : 1, UNITS = MODE == M_AFF ? 1 : 2;
+    static constexpr int PARTS = MODE == M_NV ? 2 : 1, UNITS = MODE == M_A4 ? 1 : 2;
     float s[PARTS][2][UNITS];  // [part of a unit][row][unit]
     float b[2][UNITS];
 };
@@ -195,6 +346,8 @@ __device__ __forceinline__ void load_scales(Scales<MODE> &S, uint32_t a, uint32_
             if constexpr (affine(MODE)) {
                 S.s[0][h][u] = bf16_bits_to_f32(lds16(at));
                 S.b[h][u] = bf16_bits_to_f32(lds16(at + tob));
+            } else if constexpr (codebook(MODE)) {
+                S.s[0][h][u] = f16_bits_to_f32(lds16(at));
             } else if constexpr (MODE == M_MX) {
                 S.s[0][h][u] = e8m0_to_f32(lds8(at));
             } else {
@@ -206,25 +359,24 @@ __device__ __forceinline__ void load_scales(Scales<MODE> &S, uint32_t a, uint32_
 
 // 16 rows x 4 units: wa, wb the lane's unit of rows r and r + 8.
 template <int MODE, int NB>
-__device__ __forceinline__ void tile_step(const uint4 wa, const uint4 wb, const uint32_t (&B)[NB][16],
-                                          const float (&f)[NB][2], const float (&xs)[NB][2], const Scales<MODE> &C,
-                                          float (&acc)[NB][2]) {
-    const uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w}, b[4] = {wb.x, wb.y, wb.z, wb.w};
-    constexpr int PARTS = Scales<MODE>::PARTS, WPP = 4 / PARTS;  // words a part
+__device__ __forceinline__ void tile_step(const uint32_t (&wa)[words(MODE)], const uint32_t (&wb)[words(MODE)],
+                                          const Table<MODE> &T, const uint32_t (&B)[NB][16], const float (&f)[NB][2],
+                                          const float (&xs)[NB][2], const Scales<MODE> &C, float (&acc)[NB][2]) {
+    constexpr int PARTS = Scales<MODE>::PARTS, QPP = 4 / PARTS;  // quarters of a unit in a part
 #pragma unroll
     for (int h = 0; h < PARTS; h++) {
         float c[NB][4];
 #pragma unroll
-        for (int i = 0; i < WPP; i++) {
-            const int w = h * WPP + i;
+        for (int i = 0; i < QPP; i++) {
+            const int t = h * QPP + i;
             uint32_t pa[4], pb[4];
-            expand<affine(MODE)>(a[w], pa);
-            expand<affine(MODE)>(b[w], pb);
+            expand<MODE>(wa, t, T, pa);
+            expand<MODE>(wb, t, T, pb);
 #pragma unroll
             for (int n = 0; n < NB; n++) {
-                if (i == 0) mma0(c[n], pa[0], pb[0], pa[1], pb[1], B[n][4 * w], B[n][4 * w + 1]);
-                else mma(c[n], pa[0], pb[0], pa[1], pb[1], B[n][4 * w], B[n][4 * w + 1]);
-                mma(c[n], pa[2], pb[2], pa[3], pb[3], B[n][4 * w + 2], B[n][4 * w + 3]);
+                if (i == 0) mma0(c[n], pa[0], pb[0], pa[1], pb[1], B[n][4 * t], B[n][4 * t + 1]);
+                else mma(c[n], pa[0], pb[0], pa[1], pb[1], B[n][4 * t], B[n][4 * t + 1]);
+                mma(c[n], pa[2], pb[2], pa[3], pb[3], B[n][4 * t + 2], B[n][4 * t + 3]);
             }
         }
 #pragma unroll
@@ -232,19 +384,19 @@ __device__ __forceinline__ void tile_step(const uint4 wa, const uint4 wb, const 
 #pragma unroll
             for (int k = 0; k < 2; k++) {
                 const float c0 = c[n][2 * k], c1 = c[n][2 * k + 1];
-                if constexpr (MODE == M_AFF)
+                if constexpr (MODE == M_A4)
                     acc[n][k] = fmaf(C.s[0][k][0], fmaf(c0, f[n][0], c1 * f[n][1]), acc[n][k]);
                 else
                     acc[n][k] = fmaf(C.s[h][k][0], c0 * f[n][0],
                                      fmaf(C.s[h][k][Scales<MODE>::UNITS - 1], c1 * f[n][1], acc[n][k]));
             }
     }
-    if constexpr (MODE == M_AFF) {
+    if constexpr (MODE == M_A4) {
 #pragma unroll
         for (int n = 0; n < NB; n++)
 #pragma unroll
             for (int k = 0; k < 2; k++) acc[n][k] = fmaf(C.b[k][0], xs[n][0] + xs[n][1], acc[n][k]);
-    } else if constexpr (MODE == M_AFF1) {
+    } else if constexpr (affine(MODE)) {
 #pragma unroll
         for (int n = 0; n < NB; n++)
 #pragma unroll
@@ -253,12 +405,12 @@ __device__ __forceinline__ void tile_step(const uint4 wa, const uint4 wb, const 
     }
 }
 
-// One step of T tiles: st the stage's address for this lane (+ 16 lane), sc that of row r's
+// One step of T tiles: st the stage's address for this lane (+ lane pieces), sc that of row r's
 // scales of the first tile (tot bytes on to the next tile's), `on` bytes past at the images.
 template <int MODE, int PLANES, int NB, int T>
 __device__ __forceinline__ void step(uint32_t st, uint32_t sc, uint32_t tot, uint32_t to8, uint32_t tob, uint32_t i,
-                                     uint32_t d, const StepAt<NB> &at, uint32_t on, uint32_t lane,
-                                     float (&acc)[T][NB][2]) {
+                                     uint32_t d, uint32_t word_codes, const Table<MODE> &tab, const StepAt<NB> &at,
+                                     uint32_t on, uint32_t lane, float (&acc)[T][NB][2]) {
     uint32_t B[NB][16];
     float f[NB][2], xs[NB][2];
     const bool odd_plane = PLANES == 2 && (lane & 2u);
@@ -278,17 +430,27 @@ __device__ __forceinline__ void step(uint32_t st, uint32_t sc, uint32_t tot, uin
     }
 #pragma unroll
     for (uint32_t t = 0; t < T; t++) {
-        const uint4 wa = lds128(st + t * 1024u), wb = lds128(st + t * 1024u + 512u);
+        uint32_t wa[words(MODE)], wb[words(MODE)];
+        load_unit<MODE>(st + 2u * t * rows8(MODE), wa);
+        load_unit<MODE>(st + (2u * t + 1u) * rows8(MODE), wb);
+        join_words<MODE>(wa, word_codes);
+        join_words<MODE>(wb, word_codes);
         Scales<MODE> C;
         load_scales<MODE>(C, sc + t * tot, to8, tob, i, d);
-        tile_step<MODE, NB>(wa, wb, B, f, xs, C, acc[t]);
+        tile_step<MODE, NB>(wa, wb, tab, B, f, xs, C, acc[t]);
     }
+}
+
+// Codes of a 3-bit word that come before unit u.
+template <int MODE>
+__device__ __forceinline__ uint32_t codes_before(uint32_t u) {
+    return MODE == M_CB3 ? 32u * u % 10u : 0u;
 }
 
 // Byte of unit u's entry in a row's scales.
 template <int MODE>
 __device__ __forceinline__ uint32_t scale_entry(uint32_t u, uint32_t gshift) {
-    return affine(MODE) ? (u >> gshift) * 2u : MODE == M_NV ? 2u * u : u;
+    return affine(MODE) || codebook(MODE) ? (u >> gshift) * 2u : MODE == M_NV ? 2u * u : u;
 }
 
 // ------------------------------------------------------------------- routing
@@ -337,7 +499,8 @@ struct FewParams {
     uint32_t m, R, S, E, H, I;       // H hidden, I inter
     uint32_t g1, g2, gshift1, gshift2;  // groups of a row; log2(units of 32 a group)
     int x_dtype, out_dtype, bias1_dtype, bias2_dtype, act;
-    int scale2_kind, down_affine;    // 1: the down projection is NVFP4 (scale2 in a2); affine
+    uint32_t rb1, rb2;               // bytes of a packed row
+    int scale2_kind, down_order;     // 1: the down projection is NVFP4 (scale2 in a2); order of h's values
     uint32_t split, max_parts, slots;  // mlp_down: CTAs that share 16 columns, parts an expert, scale slots
     float *partial;                  // [split][m][H] sums of mlp_down's CTAs, where they share columns
     uint32_t *arrived;               // [H / 16], zeroed by mlp_up
@@ -355,7 +518,7 @@ __device__ __forceinline__ float4 load_x4(const void *x, int dt, size_t i) {
 }
 
 // A warp writes one step image: lane l holds values 4l .. 4l+3 (unit l / 8).
-template <bool AFFINE, int PLANES>
+template <int MODE, int PLANES>
 __device__ __forceinline__ void write_step(uint8_t *dst, float4 v, uint32_t lane) {
     const uint32_t M = 0x7FFFFFFFu;
     uint32_t mb = max(max(__float_as_uint(v.x) & M, __float_as_uint(v.y) & M),
@@ -364,11 +527,11 @@ __device__ __forceinline__ void write_step(uint8_t *dst, float4 v, uint32_t lane
 #pragma unroll
     for (int d = 1; d < 8; d <<= 1) {
         mb = max(mb, __shfl_xor_sync(FULL, mb, d));
-        if constexpr (AFFINE) sum += __shfl_xor_sync(FULL, sum, d);
+        if constexpr (affine(MODE)) sum += __shfl_xor_sync(FULL, sum, d);
     }
     float scale, factor;
     unit_scale(mb, scale, factor);
-    if constexpr (AFFINE) {
+    if constexpr (order_of(MODE) == 1) {
         // a word's pairs are (0, 4), (1, 5) for the even lane and (2, 6), (3, 7) for the odd one
         const bool odd = lane & 1u;
         const float s0 = odd ? v.x : v.z, s1 = odd ? v.y : v.w;
@@ -376,6 +539,8 @@ __device__ __forceinline__ void write_step(uint8_t *dst, float4 v, uint32_t lane
         const float sixteenth = scale * 0.0625f;
         v = odd ? make_float4(r0 * scale, v.z * scale, r1 * sixteenth, v.w * sixteenth)
                 : make_float4(v.x * scale, r0 * scale, v.y * sixteenth, r1 * sixteenth);
+    } else if constexpr (order_of(MODE) == 2) {
+        v = make_float4(v.x * scale, v.z * scale, v.y * scale, v.w * scale);
     } else {
         v = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
     }
@@ -403,7 +568,7 @@ __device__ __forceinline__ void write_step(uint8_t *dst, float4 v, uint32_t lane
 template <int MODE, int PLANES, int NB>
 __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const FewParams P) {
     constexpr uint32_t PP = 2 * NB / PLANES;  // pairs a pass
-    constexpr uint32_t STAGE = UP_TILES * 2 * 512, XSTEP = step_bytes(PLANES);
+    constexpr uint32_t STAGE = UP_TILES * 2 * rows8(MODE), XSTEP = step_bytes(PLANES);
     extern __shared__ __align__(16) uint8_t sm[];
     __shared__ __align__(16) uint8_t zeros[64];
     __shared__ float red[UP_PARTS * PP * 64];  // [part][pair][gate / up][32 columns]
@@ -436,26 +601,26 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const Few
 
     const uint32_t r = lane >> 2, q = lane & 3u, tp = warp & 1u, part = warp >> 1;
     const uint32_t nu = P.H / 32u, steps = (nu + 3u) / 4u, units = P.I / 32u;
-    const uint32_t row_bytes = P.H / 2u, srow = scale_bytes(affine(MODE), P.g1), sblock = 32u * srow;
+    const uint32_t row_bytes = P.rb1, srow = scale_bytes(MODE, P.g1), sblock = 32u * srow;
     uint8_t *const images = sm + FEW_WARPS * RING * STAGE;  // [pair][step]
     uint8_t *const scales = images + PP * steps * XSTEP;    // [2][gate, up scales, biases][32 rows]
     const uint32_t sm0 = ptx::smem_u32(sm), ring = sm0 + warp * RING * STAGE;
     const uint32_t sc0 = ptx::smem_u32(scales), sbytes = sblock * (affine(MODE) ? 4u : 2u);
     const size_t up = (size_t)P.I * row_bytes, next = 8u * (size_t)row_bytes;
 
-    // requests of weights: unit, step, slot; the lane's unit of its rows
+    // requests of weights: unit, step, slot; the lane's row of the first tile
     const uint8_t *wrow = nullptr;
     uint32_t iu = 0, ij = 0, is = 0;
     auto issue = [&]() {
         if (iu < units) {
-            const uint32_t size = 4u * ij + q < nu ? 16u : 0u;  // past the row nothing is read, zeros are stored
-            const uint8_t *g = wrow + (size ? ij * 64u : 0u);
-            const uint32_t st = ring + is + lane * 16u;
-            ptx::cp_async_16(st, g, size);
-            ptx::cp_async_16(st + 512u, g + up, size);
+            const uint32_t in = 4u * ij + q < nu;  // past the row nothing is read, zeros are stored
+            const uint8_t *g = wrow + (in ? unit_byte<MODE>(4u * ij + q) : 0u);
+            const uint32_t st = ring + is + lane * piece(MODE);
+            copy_unit<MODE>(st, g, in);
+            copy_unit<MODE>(st + rows8(MODE), g + up, in);
             g += next;
-            ptx::cp_async_16(st + 1024u, g, size);
-            ptx::cp_async_16(st + 1536u, g + up, size);
+            copy_unit<MODE>(st + 2u * rows8(MODE), g, in);
+            copy_unit<MODE>(st + 3u * rows8(MODE), g + up, in);
             is = is + STAGE == RING * STAGE ? 0u : is + STAGE;
             ij += UP_PARTS;
             if (ij >= steps) {
@@ -483,7 +648,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const Few
         iu = part < steps ? blockIdx.x : units;
         ij = part;
         is = 0u;
-        wrow = P.w1 + ((size_t)e * 2u * P.I + iu * 32u + 16u * tp + r) * row_bytes + q * 16u;
+        wrow = P.w1 + ((size_t)e * 2u * P.I + iu * 32u + 16u * tp + r) * row_bytes;
         issue_scales(blockIdx.x, 0u);
 #pragma unroll
         for (uint32_t i = 0; i < RING; i++) {
@@ -492,6 +657,8 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const Few
         }
     };
     restart();
+    Table<MODE> tab;
+    tab.load(P.a1);
     __syncthreads();  // pairs[]
 
     for (uint32_t pb = 0; pb < np; pb += PP) {
@@ -503,7 +670,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const Few
             for (uint32_t j = warp; j < steps; j += FEW_WARPS) {
                 const float4 v = j * 128u + 4u * lane < P.H ? load_x4(P.x, P.x_dtype, xrow + j * 128u)
                                                             : make_float4(0.f, 0.f, 0.f, 0.f);
-                write_step<affine(MODE), PLANES>(images + (p * steps + j) * XSTEP, v, lane);
+                write_step<MODE, PLANES>(images + (p * steps + j) * XSTEP, v, lane);
             }
         }
         // what the epilogue of this warp's pair needs, requested now (a pass has at most 8)
@@ -534,8 +701,9 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const Few
                 wait_groups<RING - 1>();
                 const uint32_t u0 = tmin<uint32_t>(4u * j + 2u * (q & 1u), nu - 1u), u1 = tmin<uint32_t>(u0 + 1u, nu - 1u);
                 const uint32_t i = scale_entry<MODE>(u0, P.gshift1);
-                step<MODE, PLANES, NB, UP_TILES>(ring + slot + lane * 16u, sc, 8u * srow, sblock, 2u * sblock, i,
-                                                 scale_entry<MODE>(u1, P.gshift1) - i, at, on, lane, acc);
+                step<MODE, PLANES, NB, UP_TILES>(ring + slot + lane * piece(MODE), sc, 8u * srow, sblock, 2u * sblock, i,
+                                                 scale_entry<MODE>(u1, P.gshift1) - i, codes_before<MODE>(4u * j + q),
+                                                 tab, at, on, lane, acc);
                 on += UP_PARTS * XSTEP;
                 slot = slot + STAGE == RING * STAGE ? 0u : slot + STAGE;
                 issue();
@@ -580,8 +748,8 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const Few
                 float scale, factor;
                 unit_scale(__reduce_max_sync(FULL, __float_as_uint(h) & 0x7FFFFFFFu), scale, factor);
                 h *= scale;
-                if (b_sixteenth(P.down_affine, lane)) h *= 0.0625f;
-                uint16_t *dst = (uint16_t *)(img + un * 64u) + b_place(P.down_affine, lane);
+                if (P.down_order == 1 && (lane & 1u)) h *= 0.0625f;  // meets a 16-fold pair
+                uint16_t *dst = (uint16_t *)(img + un * 64u) + b_place(P.down_order, lane);
                 for (int k = 0; k < planes; k++, dst += 128) {
                     const __half b = __float2half_rn(h);
                     *dst = __half_as_ushort(b);
@@ -611,7 +779,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const Few
 template <int MODE, int NPL, int NB, int T>
 __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const FewParams P) {
     constexpr uint32_t PP = 2 * NB / NPL, C = 16 * T;  // pairs a pass, columns
-    constexpr uint32_t HSTEP = step_bytes(NPL), HAT = T * 2 * 512, STAGE = HAT + PP * HSTEP;
+    constexpr uint32_t HSTEP = step_bytes(NPL), HAT = T * 2 * rows8(MODE), STAGE = HAT + PP * HSTEP;
     extern __shared__ __align__(16) uint8_t sm[];
     __shared__ __align__(16) uint8_t zeros[64];
     __shared__ uint32_t mask[32], base[33], ids_s[FEW_MAX_R], first[FEW_MAX_R + 1], pairs[FEW_MAX_R],
@@ -633,7 +801,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const F
         experts[rank] = id;
         for (uint32_t t = 0; t < tid; t++) place += ids_s[t] == id;
     }
-    const uint32_t srow = scale_bytes(affine(MODE), P.g2), sslot = C * srow * (affine(MODE) ? 2u : 1u);
+    const uint32_t srow = scale_bytes(MODE, P.g2), sslot = C * srow * (affine(MODE) ? 2u : 1u);
     const uint32_t warp_bytes = RING * STAGE + P.slots * sslot;
     float *const ysm = (float *)(sm + FEW_WARPS * warp_bytes);  // [warp][token][C]
     for (uint32_t o = tid; o < FEW_WARPS * P.m * C; o += FEW_THREADS) ysm[o] = 0.f;
@@ -657,7 +825,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const F
     __syncthreads();
 
     const uint32_t r = lane >> 2, q = lane & 3u;
-    const uint32_t nu = P.I / 32u, steps = (nu + 3u) / 4u, row_bytes = P.I / 2u;
+    const uint32_t nu = P.I / 32u, steps = (nu + 3u) / 4u, row_bytes = P.rb2;
     const uint32_t row0 = blockIdx.x * C, warps = P.split * FEW_WARPS;
     // an expert is one item where there are enough for the warps
     const uint32_t parts = D == 0u || D >= warps ? 1u : tmin<uint32_t>((warps + D - 1u) / D, P.max_parts);
@@ -699,7 +867,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const F
     auto start_w = [&](const Pos &p) {
         if (p.x >= D) return;
         const size_t row = (size_t)experts[p.x] * P.H + row0;
-        w0 = P.w2 + (row + r) * row_bytes + q * 16u;  // the lane's unit of row r, step 0
+        w0 = P.w2 + (row + r) * row_bytes;  // the lane's row of the first tile
         if (p.pb == 0u) {
             const uint8_t *s = P.s2 + row * srow, *b = P.a2 + row * srow;
             for (uint32_t o = lane * 16u; o < C * srow; o += 512u) {
@@ -709,11 +877,11 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const F
         }
     };
     auto issue_w = [&](const Pos &p, uint32_t stage) {
-        const uint32_t size = 4u * p.j + q < nu ? 16u : 0u;
-        const uint8_t *src = w0 + (size ? p.j * 64u : 0u);
-        const uint32_t st = ring + stage + lane * 16u;
+        const uint32_t in = 4u * p.j + q < nu;
+        const uint8_t *src = w0 + (in ? unit_byte<MODE>(4u * p.j + q) : 0u);
+        const uint32_t st = ring + stage + lane * piece(MODE);
 #pragma unroll
-        for (uint32_t t = 0; t < 2 * T; t++, src += 8u * row_bytes) ptx::cp_async_16(st + t * 512u, src, size);
+        for (uint32_t t = 0; t < 2 * T; t++, src += 8u * (size_t)row_bytes) copy_unit<MODE>(st + t * rows8(MODE), src, in);
     };
     uint32_t ho[PP];  // the pairs' offsets in hf
     auto start_h = [&](const Pos &p) {
@@ -765,6 +933,8 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const F
     for (int t = 0; t < T; t++)
 #pragma unroll
         for (int n = 0; n < NB; n++) acc[t][n][0] = acc[t][n][1] = 0.f;
+    Table<MODE> tab;
+    tab.load(P.a2);
     const StepAt<NB> sa = step_at<NPL, NB>(ring + HAT, HSTEP, ptx::smem_u32(zeros), lane);
     uint32_t stage = 0;
     while (at.x < D) {
@@ -772,8 +942,9 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const F
         __syncwarp();             // and the other lanes' parts of the scales and of h
         const uint32_t u0 = tmin<uint32_t>(4u * at.j + 2u * (q & 1u), nu - 1u), u1 = tmin<uint32_t>(u0 + 1u, nu - 1u);
         const uint32_t i = scale_entry<MODE>(u0, P.gshift2);
-        step<MODE, NPL, NB, T>(ring + stage + lane * 16u, sslots + at.slot + r * srow, 16u * srow, 8u * srow, C * srow, i,
-                               scale_entry<MODE>(u1, P.gshift2) - i, sa, stage, lane, acc);
+        step<MODE, NPL, NB, T>(ring + stage + lane * piece(MODE), sslots + at.slot + r * srow, 16u * srow, 8u * srow,
+                               C * srow, i, scale_entry<MODE>(u1, P.gshift2) - i, codes_before<MODE>(4u * at.j + q), tab,
+                               sa, stage, lane, acc);
         const uint32_t pfirst = at.first + at.pb, pcnt = at.cnt - at.pb;
         const bool ended = advance(at);
         __syncwarp();  // every lane has read its stage and scales
@@ -864,23 +1035,23 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const F
 // ------------------------------------------------------------------ launches
 
 // Shared memory of the two kernels.
-size_t up_bytes(bool aff, uint32_t H, uint32_t groups, int planes, uint32_t blocks) {
-    return FEW_WARPS * RING * UP_TILES * 1024ull +
+size_t up_bytes(int mode, uint32_t H, uint32_t groups, int planes, uint32_t blocks) {
+    return FEW_WARPS * RING * UP_TILES * 2ull * rows8(mode) +
            (size_t)(2u * blocks / planes) * ((H / 32u + 3u) / 4u) * step_bytes(planes) +
-           128ull * scale_bytes(aff, groups) * (aff ? 2u : 1u);
+           128ull * scale_bytes(mode, groups) * (affine(mode) ? 2u : 1u);
 }
 // mlp_down: an item has steps / max_parts steps or more; RING steps ahead reach so many more.
 uint32_t down_parts(uint32_t steps) { return steps >= 4u ? steps / 2u : 1u; }
 uint32_t down_slots(uint32_t steps) { return RING / (steps / down_parts(steps)) + 2u; }
-size_t down_bytes(bool aff, uint32_t I, uint32_t groups, int planes, uint32_t blocks, uint32_t tiles, uint32_t m) {
-    return FEW_WARPS * (RING * (1024ull * tiles + (2u * blocks / planes) * step_bytes(planes)) +
-                        down_slots((I / 32u + 3u) / 4u) * 16ull * tiles * scale_bytes(aff, groups) * (aff ? 2u : 1u) +
-                        64ull * tiles * m);
+size_t down_bytes(int mode, uint32_t I, uint32_t groups, int planes, uint32_t blocks, uint32_t tiles, uint32_t m) {
+    const uint32_t slot = 16u * tiles * scale_bytes(mode, groups) * (affine(mode) ? 2u : 1u);
+    return FEW_WARPS * (RING * (2ull * rows8(mode) * tiles + (2u * blocks / planes) * step_bytes(planes)) +
+                        down_slots((I / 32u + 3u) / 4u) * (uint64_t)slot + 64ull * tiles * m);
 }
 
 template <int MODE, int PLANES, int NB>
 cudaError_t up_t(const FewParams &P, cudaStream_t st) {
-    const size_t smem = up_bytes(affine(MODE), P.H, P.g1, PLANES, NB);
+    const size_t smem = up_bytes(MODE, P.H, P.g1, PLANES, NB);
     auto kern = mlp_up<MODE, PLANES, NB>;
     static int smem_set[64];
     const cudaError_t e = ensure_dyn_smem(kern, smem, smem_set);
@@ -895,7 +1066,7 @@ cudaError_t up_t(const FewParams &P, cudaStream_t st) {
 
 template <int MODE, int NPL, int NB, int T>
 cudaError_t down_t(FewParams P, cudaStream_t st) {
-    const size_t smem = down_bytes(affine(MODE), P.I, P.g2, NPL, NB, T, P.m);
+    const size_t smem = down_bytes(MODE, P.I, P.g2, NPL, NB, T, P.m);
     auto kern = mlp_down<MODE, NPL, NB, T>;
     static int smem_set[64];
     const cudaError_t e = ensure_dyn_smem(kern, smem, smem_set);
@@ -929,7 +1100,7 @@ uint32_t blocks_a_pass(const FewParams &P, uint32_t planes) {
 template <int MODE, int PLANES>
 cudaError_t up_p(const FewParams &P, cudaStream_t st) {
     uint32_t blocks = blocks_a_pass(P, PLANES);
-    while (blocks > 1u && up_bytes(affine(MODE), P.H, P.g1, PLANES, blocks) > FEW_SMEM) blocks /= 2u;
+    while (blocks > 1u && up_bytes(MODE, P.H, P.g1, PLANES, blocks) > FEW_SMEM) blocks /= 2u;
     switch (blocks) {
         case 1: return up_t<MODE, PLANES, 1>(P, st);
         case 2: return up_t<MODE, PLANES, 2>(P, st);
@@ -943,7 +1114,7 @@ cudaError_t down_p(const FewParams &P, cudaStream_t st) {
     // share a step's B registers and its loop
     if (P.R <= FEW_ALONE_R) return down_t<MODE, NPL, 1, 1>(P, st);
     uint32_t blocks = blocks_a_pass(P, NPL);
-    while (blocks > 1u && down_bytes(affine(MODE), P.I, P.g2, NPL, blocks, 2, P.m) > FEW_SMEM) blocks /= 2u;
+    while (blocks > 1u && down_bytes(MODE, P.I, P.g2, NPL, blocks, 2, P.m) > FEW_SMEM) blocks /= 2u;
     switch (blocks) {
         case 1: return down_t<MODE, NPL, 1, 2>(P, st);
         case 2: return down_t<MODE, NPL, 2, 2>(P, st);
@@ -960,17 +1131,48 @@ cudaError_t down_m(const FewParams &P, cudaStream_t st) {
     return h_planes(P.out_dtype) == 1 ? down_p<MODE, 1>(P, st) : down_p<MODE, 2>(P, st);
 }
 
+cudaError_t launch_up(const FewParams &P, int mode, cudaStream_t st) {
+    switch (mode) {
+        case M_A4: return up_m<M_A4>(P, st);
+        case M_A4U: return up_m<M_A4U>(P, st);
+        case M_A6: return up_m<M_A6>(P, st);
+        case M_A8: return up_m<M_A8>(P, st);
+        case M_NV: return up_m<M_NV>(P, st);
+        case M_MX: return up_m<M_MX>(P, st);
+        case M_CB2: return up_m<M_CB2>(P, st);
+        case M_CB3: return up_m<M_CB3>(P, st);
+        default: return up_m<M_CB4>(P, st);
+    }
+}
+
+cudaError_t launch_down(const FewParams &P, int mode, cudaStream_t st) {
+    switch (mode) {
+        case M_A4: return down_m<M_A4>(P, st);
+        case M_A4U: return down_m<M_A4U>(P, st);
+        case M_A6: return down_m<M_A6>(P, st);
+        case M_A8: return down_m<M_A8>(P, st);
+        case M_NV: return down_m<M_NV>(P, st);
+        case M_MX: return down_m<M_MX>(P, st);
+        case M_CB2: return down_m<M_CB2>(P, st);
+        case M_CB3: return down_m<M_CB3>(P, st);
+        default: return down_m<M_CB4>(P, st);
+    }
+}
+
 // The mode of a projection, or -1.
 int mode_of(const moe_expert_weights &w, uint32_t k) {
     const int kind = kind_of((int)w.fmt, (int)w.bits);
     if (k % 32u != 0 || (((uintptr_t)w.packed | (uintptr_t)w.scales) & 15u)) return -1;
-    if (kind == K_AFF4) {
-        const uint32_t u = w.group_size / 32u;  // units a group
-        if (w.group_size % 32u != 0 || (u & (u - 1u)) != 0 || ((uintptr_t)w.aux & 15u)) return -1;
-        return u == 1u ? M_AFF1 : M_AFF;
-    }
     if (kind == K_NVFP4) return ((uintptr_t)w.aux & 3u) ? -1 : M_NV;
-    return kind == K_MXFP4 ? M_MX : -1;
+    if (kind == K_MXFP4) return M_MX;
+    const uint32_t u = w.group_size / 32u;  // units a group
+    if (w.group_size % 32u != 0 || (u & (u - 1u)) != 0) return -1;
+    if (w.fmt == MOE_FMT_AFFINE) {
+        if ((uintptr_t)w.aux & 15u) return -1;
+        return kind == K_AFF4 ? (u == 1u ? M_A4U : M_A4) : kind == K_AFF6 ? M_A6 : M_A8;
+    }
+    if ((uintptr_t)w.aux & 1u) return -1;
+    return kind == K_CB2 ? M_CB2 : kind == K_CB3 ? M_CB3 : M_CB4;
 }
 
 uint32_t log2_units(const moe_expert_weights &w) {
@@ -1002,8 +1204,8 @@ bool mlp_few_supported(const MlpArgs &a) {
     if (R > FEW_MAX_R || a.m > FEW_MAX_TOKENS || a.E > MOE_ROUTE_MAX_EXPERTS) return false;
     const int m1 = mode_of(*a.gate_up, a.hidden), m2 = mode_of(*a.down, a.inter);
     if (m1 < 0 || m2 < 0 || ((uintptr_t)a.x & 15u)) return false;
-    return up_bytes(affine(m1), a.hidden, a.hidden / a.gate_up->group_size, x_planes(a.x_dtype), 1) <= FEW_SMEM &&
-           down_bytes(affine(m2), a.inter, a.inter / a.down->group_size, h_planes(a.out_dtype), 1, 2, a.m) <=
+    return up_bytes(m1, a.hidden, a.hidden / a.gate_up->group_size, x_planes(a.x_dtype), 1) <= FEW_SMEM &&
+           down_bytes(m2, a.inter, a.inter / a.down->group_size, h_planes(a.out_dtype), 1, 2, a.m) <=
                FEW_SMEM;
 }
 
@@ -1025,20 +1227,15 @@ cudaError_t launch_mlp_few(const MlpArgs &a, uint32_t *err, void *hf, cudaStream
     P.x_dtype = a.x_dtype; P.out_dtype = a.out_dtype; P.act = a.act;
     const int m1 = mode_of(*a.gate_up, a.hidden), m2 = mode_of(*a.down, a.inter);
     P.scale2_kind = m2 == M_NV;
-    P.down_affine = affine(m2);
+    P.down_order = m2 == M_A4 || m2 == M_A4U ? 1 : m2 == M_A8 ? 2 : 0;
+    P.rb1 = (uint32_t)moe_packed_row_bytes(a.gate_up->fmt, a.gate_up->bits, a.hidden);
+    P.rb2 = (uint32_t)moe_packed_row_bytes(a.down->fmt, a.down->bits, a.inter);
     // mlp_down's CTAs: up to one wave of two an SM (a second wave would pay its prologue
     // again: 58 us against 62 with 3 and 4 CTAs a block of 88, 61 against 64 with 2 and 4
     // of 128); a token or two have too little work to be worth the join
     P.split = P.R <= FEW_ALONE_R ? 1u : tmin<uint32_t>(tmax<uint32_t>(2u * SMS / (P.H / 32u), 1u), MAX_SPLIT);
-    const cudaError_t ce = m1 == M_AFF    ? up_m<M_AFF>(P, st)
-                           : m1 == M_AFF1 ? up_m<M_AFF1>(P, st)
-                           : m1 == M_NV   ? up_m<M_NV>(P, st)
-                                          : up_m<M_MX>(P, st);
-    if (ce != cudaSuccess) return ce;
-    return m2 == M_AFF    ? down_m<M_AFF>(P, st)
-           : m2 == M_AFF1 ? down_m<M_AFF1>(P, st)
-           : m2 == M_NV   ? down_m<M_NV>(P, st)
-                          : down_m<M_MX>(P, st);
+    const cudaError_t ce = launch_up(P, m1, st);
+    return ce == cudaSuccess ? launch_down(P, m2, st) : ce;
 }
 
 }  // namespace moe
