@@ -39,7 +39,8 @@ namespace {
 
 constexpr uint32_t FULL = 0xFFFFFFFFu;
 constexpr uint32_t FEW_THREADS = 256, FEW_WARPS = 8;
-constexpr uint32_t FEW_MAX_R = 256;      // pairs (one thread each in the prologues)
+constexpr uint32_t FEW_MAX_R = 512;      // pairs
+constexpr uint32_t ID_LOOPS = FEW_MAX_R / FEW_THREADS;  // a thread's in the prologues
 constexpr uint32_t FEW_MAX_TOKENS = 64;  // rows of mlp_down's per-warp sums
 constexpr uint32_t RING = 3;             // steps of a warp in flight
 constexpr uint32_t UP_TILES = 2;         // mlp_up: tiles of 16 rows a warp works on at once
@@ -455,13 +456,18 @@ __device__ __forceinline__ uint32_t scale_entry(uint32_t u, uint32_t gshift) {
 
 // ------------------------------------------------------------------- routing
 
-// The distinct valid experts of at most 256 pairs as bits, ascending ranks by prefix
-// counts. All threads of the CTA call it; shared arrays of 32 and 33.
-__device__ __forceinline__ uint32_t expert_mask(uint32_t id, bool valid, uint32_t *mask, uint32_t *base) {
+// The distinct valid experts of the pairs' ids (shared, past-the-last and invalid ones
+// FULL) as bits, ascending ranks by prefix counts. All threads of the CTA call it;
+// shared arrays of 32 and 33.
+__device__ __forceinline__ uint32_t expert_mask(const uint32_t *ids, uint32_t *mask, uint32_t *base) {
     const uint32_t tid = threadIdx.x;
     if (tid < 32) mask[tid] = 0u;
     __syncthreads();
-    if (valid) atomicOr(&mask[id >> 5], 1u << (id & 31u));
+#pragma unroll
+    for (uint32_t i = 0; i < ID_LOOPS; i++) {
+        const uint32_t id = ids[tid + i * FEW_THREADS];
+        if (id != FULL) atomicOr(&mask[id >> 5], 1u << (id & 31u));
+    }
     __syncthreads();
     if (tid < 32) {
         uint32_t n = __popc(mask[tid]), before = n;
@@ -559,9 +565,9 @@ __device__ __forceinline__ void write_step(uint8_t *dst, float4 v, uint32_t lane
     if ((lane & 7u) == 0u) *(float2 *)(dst + PLANES * 256 + (lane >> 3) * 8u) = make_float2(factor, sum);
 }
 
-// mlp_up. grid (blocks of units, pairs). A CTA works for the expert of its pair, if no
-// earlier pair has the same, on units of 32 columns of h (units of mlp_down; 64 weight
-// rows: tile t pairs gate rows 8t..8t+7 with up rows 8t..8t+7, so that a lane's two
+// mlp_up. grid (blocks of units, pairs or experts). A CTA works for the expert of its
+// pair, if no earlier pair has the same (or, with more pairs than experts, for its own
+// expert), on units of 32 columns of h (units of mlp_down; 64 weight rows: tile t pairs gate rows 8t..8t+7 with up rows 8t..8t+7, so that a lane's two
 // accumulator rows are the gate and the up of one column). Each pair of tiles has four
 // warps, which take the steps of 128 codes in turn and run on into the CTA's next unit;
 // x is written as step images once for all.
@@ -572,7 +578,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const Few
     extern __shared__ __align__(16) uint8_t sm[];
     __shared__ __align__(16) uint8_t zeros[64];
     __shared__ float red[UP_PARTS * PP * 64];  // [part][pair][gate / up][32 columns]
-    __shared__ uint32_t wcount[FEW_WARPS], pairs[FEW_MAX_R];
+    __shared__ uint32_t wcount[ID_LOOPS * FEW_WARPS], pairs[FEW_MAX_R];
 
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
     if (tid < 16) ((uint32_t *)zeros)[tid] = 0u;
@@ -580,24 +586,44 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const Few
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
 
-    const uint32_t id = tid < P.R ? __ldg(P.ids + tid) : FULL, e = __ldg(P.ids + blockIdx.y);
+    const bool by_pair = P.R <= P.E;
+    const uint32_t e = by_pair ? __ldg(P.ids + blockIdx.y) : blockIdx.y;
+    uint32_t id[ID_LOOPS];
+#pragma unroll
+    for (uint32_t i = 0; i < ID_LOOPS; i++) {
+        const uint32_t p = tid + i * FEW_THREADS;
+        id[i] = p < P.R ? __ldg(P.ids + p) : FULL;
+    }
     if (blockIdx.x == 0 && blockIdx.y == 0) {
-        if (tid < P.R && id >= P.E) atomicOr(P.err, ERR_BAD_ID);
+#pragma unroll
+        for (uint32_t i = 0; i < ID_LOOPS; i++)
+            if (tid + i * FEW_THREADS < P.R && id[i] >= P.E) atomicOr(P.err, ERR_BAD_ID);
         if (P.split > 1u)
             for (uint32_t i = tid; i < P.H / 16u; i += FEW_THREADS) P.arrived[i] = 0u;
     }
     if (e >= P.E) return;
-    const bool same = id == e;
-    const uint32_t mine_w = __ballot_sync(FULL, same);
-    if (lane == 0) wcount[warp] = __popc(mine_w);
-    if (__syncthreads_or(same && tid < blockIdx.y)) return;
-    uint32_t np = 0, before = 0;
+    bool earlier = false;
+    uint32_t mine_w[ID_LOOPS];
 #pragma unroll
-    for (uint32_t i = 0; i < FEW_WARPS; i++) {
-        if (i < warp) before += wcount[i];
-        np += wcount[i];
+    for (uint32_t i = 0; i < ID_LOOPS; i++) {
+        mine_w[i] = __ballot_sync(FULL, id[i] == e);
+        if (lane == 0) wcount[i * FEW_WARPS + warp] = __popc(mine_w[i]);
+        earlier |= by_pair && id[i] == e && tid + i * FEW_THREADS < blockIdx.y;
     }
-    if (same) pairs[before + __popc(mine_w & ((1u << lane) - 1u))] = tid;
+    if (__syncthreads_or(earlier)) return;
+    uint32_t np = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < ID_LOOPS; i++) {
+        uint32_t before = np;
+#pragma unroll
+        for (uint32_t k = 0; k < FEW_WARPS; k++) {
+            const uint32_t n = wcount[i * FEW_WARPS + k];
+            if (k < warp) before += n;
+            np += n;
+        }
+        if (id[i] == e) pairs[before + __popc(mine_w[i] & ((1u << lane) - 1u))] = tid + i * FEW_THREADS;
+    }
+    if (np == 0u) return;
 
     const uint32_t r = lane >> 2, q = lane & 3u, tp = warp & 1u, part = warp >> 1;
     const uint32_t nu = P.H / 32u, steps = (nu + 3u) / 4u, units = P.I / 32u;
@@ -787,26 +813,33 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const F
 
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
     if (tid < 16) ((uint32_t *)zeros)[tid] = 0u;
-    const uint32_t id = tid < P.R ? __ldg(P.ids + tid) : FULL;  // complete before mlp_up began
-    const bool valid = id < P.E;
-    ids_s[tid] = valid ? id : FULL;
-    first[tid] = 0u;
-    if (tid == 0) first[FEW_MAX_R] = 0u;
-    const uint32_t D = expert_mask(id, valid, mask, base);
-    // pairs by expert: rank, count, first, place (stable)
-    uint32_t rank = 0, place = 0;
-    if (valid) {
-        rank = base[id >> 5] + __popc(mask[id >> 5] & ((1u << (id & 31u)) - 1u));
-        atomicAdd(&first[rank + 1u], 1u);
-        experts[rank] = id;
-        for (uint32_t t = 0; t < tid; t++) place += ids_s[t] == id;
+#pragma unroll
+    for (uint32_t i = 0; i < ID_LOOPS; i++) {
+        const uint32_t p = tid + i * FEW_THREADS;
+        const uint32_t id = p < P.R ? __ldg(P.ids + p) : FULL;  // complete before mlp_up began
+        ids_s[p] = id < P.E ? id : FULL;
+        first[p] = 0u;
     }
+    if (tid == 0) first[FEW_MAX_R] = 0u;
+    __syncthreads();
+    const uint32_t D = expert_mask(ids_s, mask, base);
     const uint32_t srow = scale_bytes(MODE, P.g2), sslot = C * srow * (affine(MODE) ? 2u : 1u);
     const uint32_t warp_bytes = RING * STAGE + P.slots * sslot;
     float *const ysm = (float *)(sm + FEW_WARPS * warp_bytes);  // [warp][token][C]
     for (uint32_t o = tid; o < FEW_WARPS * P.m * C; o += FEW_THREADS) ysm[o] = 0.f;
     __syncthreads();
     if (warp == 0) {
+        // the pairs by expert, in their order: ranks, counts, firsts, places
+        auto rank_of = [&](uint32_t id) { return base[id >> 5] + __popc(mask[id >> 5] & ((1u << (id & 31u)) - 1u)); };
+        for (uint32_t o = 0; o < P.R; o += 32) {
+            const uint32_t id = ids_s[o + lane], same = __match_any_sync(FULL, id);
+            if (id != FULL && (same & ((1u << lane) - 1u)) == 0u) {
+                const uint32_t x = rank_of(id);
+                first[x + 1u] += __popc(same);
+                experts[x] = id;
+            }
+            __syncwarp();
+        }
         uint32_t carry = 0;
         for (uint32_t o = 0; o < D; o += 32) {
             uint32_t v = o + lane < D ? first[o + lane + 1u] : 0u;
@@ -819,9 +852,23 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const F
             if (o + lane < D) first[o + lane + 1u] = v;
             carry = __shfl_sync(FULL, v, 31);
         }
+        __syncwarp();
+        for (uint32_t o = 0; o < P.R; o += 32) {  // first[x] runs to the next expert's and is put back below
+            const uint32_t id = ids_s[o + lane], same = __match_any_sync(FULL, id), before = same & ((1u << lane) - 1u);
+            const uint32_t x = id != FULL ? rank_of(id) : 0u;
+            if (id != FULL) pairs[first[x] + __popc(before)] = (o + lane) | ((o + lane) / P.S) << 16;  // pair, token
+            __syncwarp();
+            if (id != FULL && before == 0u) first[x] += __popc(same);
+            __syncwarp();
+        }
+        for (uint32_t o = (D + 31u) & ~31u; o > 0u; o -= 32) {  // from the top: first[x] = old first[x - 1]'s end
+            const uint32_t x = o - 32u + lane;
+            const uint32_t v = x < D && x > 0u ? first[x - 1u] : 0u;
+            __syncwarp();
+            if (x < D) first[x] = v;
+            __syncwarp();
+        }
     }
-    __syncthreads();
-    if (valid) pairs[first[rank] + place] = tid | (tid / P.S) << 16;  // pair, token
     __syncthreads();
 
     const uint32_t r = lane >> 2, q = lane & 3u;
@@ -1060,7 +1107,7 @@ cudaError_t up_t(const FewParams &P, cudaStream_t st) {
     // units of an expert follow in the same CTA, which saves it the prologue
     const uint32_t experts = tmin<uint32_t>(P.R, P.E);
     const uint32_t gx = tmin<uint32_t>((4u * SMS + experts - 1u) / experts, P.I / 32u);
-    kern<<<dim3(gx, P.R), FEW_THREADS, smem, st>>>(P);
+    kern<<<dim3(gx, experts), FEW_THREADS, smem, st>>>(P);
     return cudaGetLastError();
 }
 
@@ -1197,7 +1244,7 @@ uint64_t mlp_few_workspace(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t
 }
 
 // Whole 32-code units of 16 aligned bytes and scale groups of whole units in both
-// projections, at most 256 pairs of at most 64 tokens, x in shared memory beside the
+// projections, at most 512 pairs of at most 64 tokens, x in shared memory beside the
 // ring.
 bool mlp_few_supported(const MlpArgs &a) {
     const uint64_t R = (uint64_t)a.m * a.S;

@@ -205,6 +205,8 @@ SHAPES = [  # m, hidden, inter, top_k, E, format, down's format
     (8, 1024, 160, 8, 8, NVFP4, None), (4, 544, 96, 2, 5, MXFP4, None), (2, 200, 48, 2, 4, (FMT_AFFINE, 8, 8), None),
     (7, 256, 128, 3, 6, AFF4, AFF6), (5, 512, 256, 4, 9, CB3, NVFP4), (33, 256, 64, 6, 20, AFF4, None),
     (24, 512, 64, 2, 64, NVFP4, MXFP4), (130, 256, 128, 4, 8, AFF4, AFF8), (16, 96, 64, 4, 4, (FMT_AFFINE, 4, 32), None),
+    (64, 256, 64, 8, 40, NVFP4, None), (63, 160, 96, 8, 200, (FMT_AFFINE, 4, 32), None), (40, 128, 64, 12, 16, CB3, CB4),
+    (65, 128, 64, 2, 70, AFF6, None), (17, 192, 64, 16, 300, AFF8, CB2), (2, 4096, 128, 1, 3, CB2, AFF8),
 ]
 
 
