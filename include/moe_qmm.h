@@ -391,12 +391,23 @@ typedef struct {
  *             16-byte aligned, its first 4 bytes zero before the first use: the
  *             device error word that moe_qmm_id_poll_error reads and clears. Calls
  *             that share it must be ordered on the GPU.
- *   path      MOE_PATH_AUTO; MOE_PATH_DECODE and MOE_PATH_GROUPED make both products
- *             take that path, with moe_qmm_id_path's errors. No launch flags.
- * The two products' formats may differ. h is held in bf16 for bf16 x and in f32
- * otherwise; the products and the sum are accumulated in f32 and out is rounded
- * once. Errors as moe_qmm_id_glu and moe_combine.
+ *   path      MOE_PATH_AUTO, or MOE_PATH_DECODE (the few-token kernels wherever they
+ *             apply) or MOE_PATH_GROUPED (never those). No launch flags.
+ * The two products' formats may differ. Few tokens (at most MOE_MLP_FEW_TOKENS, with
+ * at most MOE_MLP_FEW_PAIRS pairs; under AUTO at most 64 pairs or 4 an expert) take
+ * two kernels, the second of which sums over the slots, where hidden and inter are
+ * multiples of 32, affine and codebook groups powers of two >= 32, and packed,
+ * scales, aux (affine) and x are 16-byte aligned. Otherwise moe_qmm_id_glu's and
+ * moe_qmm_id's paths run (with MOE_PATH_AUTO, DECODE or GROUPED as given), then
+ * moe_combine's kernel.
+ * h has 11 significant bits in the few-token kernels for a bf16 result and 22
+ * otherwise, under a power of two for each 32 values; elsewhere it is bf16 for bf16 x
+ * and f32 for f16 and f32 x. The products and the sum are accumulated in f32 and out
+ * is rounded once. A value of x or h that is not finite makes the results that it
+ * enters not finite. Errors as moe_qmm_id_glu and moe_combine.
  */
+#define MOE_MLP_FEW_TOKENS 64u
+#define MOE_MLP_FEW_PAIRS 512u
 size_t moe_mlp_workspace_bytes(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t n_expert_used,
                                uint32_t num_experts, moe_dtype x_dtype);
 moe_status moe_mlp(const void *x, const uint32_t *ids, const float *weights, const moe_expert_weights *gate_up,

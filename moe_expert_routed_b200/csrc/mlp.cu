@@ -90,7 +90,15 @@ moe_status moe_mlp(const void *x, const uint32_t *ids, const float *weights, con
     void *h = ws + L.h, *z = ws + L.z;
     const MlpArgs a{x,      ids,   weights, gate_up,       down,        residual,     out,           m,
                     hidden, inter, n_expert_used, num_experts, (int)x_dtype, (int)out_dtype, (int)act};
-    if (path != MOE_PATH_GROUPED && mlp_few_supported(a))
+    // The few-token kernels multiply every pair with its expert's rows on mma.sync, four
+    // pairs' worth of tensor work for one, so their time grows with the pairs an expert
+    // has; the grouped GEMM's hardly does. Measured with 2,816 x 704 experts, few against
+    // grouped: at 4 pairs an expert 110 / 177 us (32 experts, affine 4 bits), 116 / 128
+    // (NVFP4), 147 / 180 (affine 8 bits); at 8 171 / 179, 179 / 131, 268 / 183. With up to 64
+    // pairs the routing and the launches of the grouped path cost more: 8 experts, 64
+    // pairs 49 / 79, 52 / 63, 66 / 83.
+    const bool few = path == MOE_PATH_DECODE || R <= 64u || R <= 4ull * num_experts;
+    if (few && path != MOE_PATH_GROUPED && mlp_few_supported(a))
         return launch_mlp_few(a, (uint32_t *)ws, h, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     const moe_dtype hd = h_dtype((int)x_dtype);
     LayerProduct layer{0u};

@@ -39,9 +39,9 @@ namespace {
 
 constexpr uint32_t FULL = 0xFFFFFFFFu;
 constexpr uint32_t FEW_THREADS = 256, FEW_WARPS = 8;
-constexpr uint32_t FEW_MAX_R = 512;      // pairs
+constexpr uint32_t FEW_MAX_R = MOE_MLP_FEW_PAIRS;
 constexpr uint32_t ID_LOOPS = FEW_MAX_R / FEW_THREADS;  // a thread's in the prologues
-constexpr uint32_t FEW_MAX_TOKENS = 64;  // rows of mlp_down's per-warp sums
+constexpr uint32_t FEW_MAX_TOKENS = MOE_MLP_FEW_TOKENS;  // rows of mlp_down's per-warp sums
 constexpr uint32_t RING = 3;             // steps of a warp in flight
 constexpr uint32_t UP_TILES = 2;         // mlp_up: tiles of 16 rows a warp works on at once
 constexpr uint32_t UP_PARTS = 4;         // mlp_up: warps that share a pair of tiles, each a part of hidden
@@ -199,7 +199,11 @@ __device__ __forceinline__ void join_words(uint32_t (&w)[words(MODE)], uint32_t 
 //   affine, as integers times 2^-24: 4 bits (0, 4), (1, 5), (2, 6), (3, 7), the second and
 //   fourth pair 16 times that; 8 bits (0, 2), (1, 3), (4, 6), (5, 7); 6 bits in order
 //   E2M1 and codebook values in order: (0, 1), (2, 3), (4, 5), (6, 7)
-template <int MODE>
+// CENTRED (affine, for f32 results): the integers less the middle of their range, which the
+// bias makes up for. The tensor core cuts products off 24 bits below the largest term,
+// and sums of codes that are all positive lose several times more of what is left once
+// the bias is added (2.3e-6 of an f32 result against 64 bits).
+template <int MODE, bool CENTRED>
 __device__ __forceinline__ void expand(const uint32_t (&w)[words(MODE)], int t, const Table<MODE> &T, uint32_t (&p)[4]) {
     if constexpr (MODE == M_A4 || MODE == M_A4U) {
         p[0] = w[t] & 0x000F000Fu;
@@ -244,12 +248,27 @@ __device__ __forceinline__ void expand(const uint32_t (&w)[words(MODE)], int t, 
         T.look(n, p[0], p[1]);
         T.look(n >> 16, p[2], p[3]);
     }
+    if constexpr (CENTRED) {
+        // 0x6400 | c is 1024 + c (1024 + 16 c a nibble higher); exact
+        constexpr uint32_t less = MODE == M_A8 ? 0xE480E480u : MODE == M_A6 ? 0xE420E420u : 0xE408E408u;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint32_t v = p[i] | 0x64006400u;
+            if ((MODE == M_A4 || MODE == M_A4U) && i % 2 == 1)
+                asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[i]) : "r"(v), "r"(0x2C002C00u), "r"(0xD480D480u));
+            else
+                asm("add.rn.f16x2 %0, %1, %2;" : "=r"(p[i]) : "r"(v), "r"(less));
+        }
+    }
 }
+constexpr bool centred(int mode, int planes) { return affine(mode) && planes == 2; }
+constexpr float middle(int mode) { return mode == M_A8 ? 128.f : mode == M_A6 ? 32.f : 8.f; }
 // What expand()'s values have to be multiplied by.
-constexpr float code_unit(int mode) { return affine(mode) ? 16777216.f : 1.f; }
+constexpr float code_unit(int mode, int planes) { return affine(mode) && !centred(mode, planes) ? 16777216.f : 1.f; }
 
 // Order of x against expand()'s pairs: 0 as it stands, 1 as 4-bit affine words part it
-// (with a sixteenth of the values that meet the 16-fold pairs), 2 as 8-bit words do.
+// (where not centred with a sixteenth of the values that meet the 16-fold pairs), 2 as
+// 8-bit words do.
 constexpr int order_of(int mode) { return mode == M_A4 || mode == M_A4U ? 1 : mode == M_A8 ? 2 : 0; }
 // Place of value c of a unit among its 32 f16 values.
 __device__ __forceinline__ uint32_t b_place(int order, uint32_t c) {
@@ -336,7 +355,7 @@ struct Scales {
 
 // a: shared address of row r's scales, to8: bytes to row r + 8, tob: to the biases; i, d:
 // bytes to the first unit's entry and on to the second's.
-template <int MODE>
+template <int MODE, bool CENTRED>
 __device__ __forceinline__ void load_scales(Scales<MODE> &S, uint32_t a, uint32_t to8, uint32_t tob, uint32_t i,
                                             uint32_t d) {
 #pragma unroll
@@ -347,6 +366,7 @@ __device__ __forceinline__ void load_scales(Scales<MODE> &S, uint32_t a, uint32_
             if constexpr (affine(MODE)) {
                 S.s[0][h][u] = bf16_bits_to_f32(lds16(at));
                 S.b[h][u] = bf16_bits_to_f32(lds16(at + tob));
+                if constexpr (CENTRED) S.b[h][u] = fmaf(middle(MODE), S.s[0][h][u], S.b[h][u]);
             } else if constexpr (codebook(MODE)) {
                 S.s[0][h][u] = f16_bits_to_f32(lds16(at));
             } else if constexpr (MODE == M_MX) {
@@ -359,7 +379,7 @@ __device__ __forceinline__ void load_scales(Scales<MODE> &S, uint32_t a, uint32_
 }
 
 // 16 rows x 4 units: wa, wb the lane's unit of rows r and r + 8.
-template <int MODE, int NB>
+template <int MODE, bool CENTRED, int NB>
 __device__ __forceinline__ void tile_step(const uint32_t (&wa)[words(MODE)], const uint32_t (&wb)[words(MODE)],
                                           const Table<MODE> &T, const uint32_t (&B)[NB][16], const float (&f)[NB][2],
                                           const float (&xs)[NB][2], const Scales<MODE> &C, float (&acc)[NB][2]) {
@@ -371,8 +391,8 @@ __device__ __forceinline__ void tile_step(const uint32_t (&wa)[words(MODE)], con
         for (int i = 0; i < QPP; i++) {
             const int t = h * QPP + i;
             uint32_t pa[4], pb[4];
-            expand<MODE>(wa, t, T, pa);
-            expand<MODE>(wb, t, T, pb);
+            expand<MODE, CENTRED>(wa, t, T, pa);
+            expand<MODE, CENTRED>(wb, t, T, pb);
 #pragma unroll
             for (int n = 0; n < NB; n++) {
                 if (i == 0) mma0(c[n], pa[0], pb[0], pa[1], pb[1], B[n][4 * t], B[n][4 * t + 1]);
@@ -415,7 +435,8 @@ __device__ __forceinline__ void step(uint32_t st, uint32_t sc, uint32_t tot, uin
     uint32_t B[NB][16];
     float f[NB][2], xs[NB][2];
     const bool odd_plane = PLANES == 2 && (lane & 2u);
-    const float unit = odd_plane ? code_unit(MODE) * 4.8828125e-4f : code_unit(MODE);  // 2^-11
+    constexpr bool CENTRED = centred(MODE, PLANES);
+    const float unit = odd_plane ? code_unit(MODE, PLANES) * 4.8828125e-4f : code_unit(MODE, PLANES);  // 2^-11
 #pragma unroll
     for (int n = 0; n < NB; n++) {
 #pragma unroll
@@ -437,8 +458,8 @@ __device__ __forceinline__ void step(uint32_t st, uint32_t sc, uint32_t tot, uin
         join_words<MODE>(wa, word_codes);
         join_words<MODE>(wb, word_codes);
         Scales<MODE> C;
-        load_scales<MODE>(C, sc + t * tot, to8, tob, i, d);
-        tile_step<MODE, NB>(wa, wb, tab, B, f, xs, C, acc[t]);
+        load_scales<MODE, CENTRED>(C, sc + t * tot, to8, tob, i, d);
+        tile_step<MODE, CENTRED, NB>(wa, wb, tab, B, f, xs, C, acc[t]);
     }
 }
 
@@ -542,7 +563,7 @@ __device__ __forceinline__ void write_step(uint8_t *dst, float4 v, uint32_t lane
         const bool odd = lane & 1u;
         const float s0 = odd ? v.x : v.z, s1 = odd ? v.y : v.w;
         const float r0 = __shfl_xor_sync(FULL, s0, 1), r1 = __shfl_xor_sync(FULL, s1, 1);
-        const float sixteenth = scale * 0.0625f;
+        const float sixteenth = centred(MODE, PLANES) ? scale : scale * 0.0625f;
         v = odd ? make_float4(r0 * scale, v.z * scale, r1 * sixteenth, v.w * sixteenth)
                 : make_float4(v.x * scale, r0 * scale, v.y * sixteenth, r1 * sixteenth);
     } else if constexpr (order_of(MODE) == 2) {
@@ -774,7 +795,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const Few
                 float scale, factor;
                 unit_scale(__reduce_max_sync(FULL, __float_as_uint(h) & 0x7FFFFFFFu), scale, factor);
                 h *= scale;
-                if (P.down_order == 1 && (lane & 1u)) h *= 0.0625f;  // meets a 16-fold pair
+                if (P.down_order == 1 && planes == 1 && (lane & 1u)) h *= 0.0625f;  // meets a 16-fold pair
                 uint16_t *dst = (uint16_t *)(img + un * 64u) + b_place(P.down_order, lane);
                 for (int k = 0; k < planes; k++, dst += 128) {
                     const __half b = __float2half_rn(h);

@@ -227,6 +227,58 @@ def test_mlp_shapes_biases_residual(shape, act):
     check(L, res, DT_BF16, r64)
 
 
+@pytest.mark.parametrize("path", ["decode", "grouped"])
+@pytest.mark.parametrize("m", [3, 24, 64])
+@pytest.mark.parametrize("fmt", ["aff4", "aff4g32", "nvfp4", "cb3", "aff6"])
+def test_mlp_paths_agree_with_the_layer(fmt, m, path):
+    """Both ways at many pairs an expert (several passes of the few-token kernels)."""
+    f, bits, gs = FORMATS[fmt]
+    L = LR.Layer(m=m, hidden=256, inter=192, top_k=3, E=4, fmt=f, bits=bits, gs=gs, x_dtype=DT_BF16, seed=m + 40)
+    layer = build(L, out_dtype=DT_BF16, path=path)
+    check(L, layer(*inputs(L)), DT_BF16)
+
+
+@pytest.mark.parametrize("x_dtype", [DT_BF16, DT_F16, DT_F32])
+@pytest.mark.parametrize("m", [1, 6])
+def test_mlp_wide_range_of_x(x_dtype, m):
+    """Units of very different sizes, zeros and subnormals: each unit has a scale of its own."""
+    L = LR.Layer(m=m, hidden=512, inter=128, top_k=4, E=8, fmt=FMT_AFFINE, bits=4, gs=64, x_dtype=x_dtype, seed=70)
+    x = torch.randn(m, 512, generator=torch.Generator().manual_seed(2), dtype=torch.float64)
+    x *= torch.exp2(torch.linspace(-30 if x_dtype != DT_F16 else -12, 6, 16)).repeat_interleave(32)
+    x[:, 64:96] = 0
+    x[:, 100:104] = 2.0**-24
+    t = x.to(LR.TORCH_DT[x_dtype])
+    bits_ = t.float().numpy() if x_dtype == DT_F32 else t.view(torch.int16).numpy().view(np.uint16)
+    L.gu = L.gu.with_x(bits_)
+    layer = build(L, out_dtype=DT_F32)
+    check(L, layer(*inputs(L)), DT_F32)
+
+
+def test_mlp_rows_do_not_mix():
+    """A token with NaN and one with infinities leave the other tokens' results alone."""
+    L = LR.Layer(m=6, hidden=256, inter=128, top_k=2, E=2, fmt=FMT_AFFINE, bits=4, gs=32, x_dtype=DT_BF16, seed=12)
+    layer = build(L, out_dtype=DT_BF16)
+    x, ids, w = inputs(L)
+    want = layer(x, ids, w)
+    x = x.clone()
+    x[1, 3] = float("nan")
+    x[4, 200] = float("inf")
+    out = layer(x, ids, w)
+    keep = [0, 2, 3, 5]
+    assert torch.equal(out[keep], want[keep])
+    assert not torch.isfinite(out[1]).any() and not torch.isfinite(out[4]).any()
+
+
+def test_mlp_leaves_other_rows_of_out_alone():
+    L = LR.Layer(m=3, hidden=128, inter=64, top_k=2, E=5, fmt=FMT_MXFP4, bits=4, gs=32, x_dtype=DT_F32, seed=13)
+    layer = build(L, out_dtype=DT_F32, max_tokens=9)
+    x, ids, w = inputs(L)
+    buf = torch.full((5, 128), 7.0, device="cuda")
+    layer(x, ids, w, out=buf[1:4])
+    check(L, buf[1:4], DT_F32)
+    assert (buf[[0, 4]] == 7.0).all()
+
+
 @pytest.mark.parametrize("m", [1, 4, 60])
 @pytest.mark.parametrize("fmt", ["aff4", "nvfp4", "cb3"])
 def test_mlp_ids_out_of_range_are_left_out(fmt, m):
