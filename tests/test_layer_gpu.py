@@ -254,6 +254,25 @@ def test_mlp_wide_range_of_x(x_dtype, m):
     check(L, layer(*inputs(L)), DT_F32)
 
 
+@pytest.mark.parametrize("fmt", sorted(FORMATS))
+@pytest.mark.parametrize("m", [1, 7])
+def test_mlp_few_tokens_keep_32_bits(fmt, m):
+    """f32 results of the few-token kernels against 64 bits, by the 2-norm.
+
+    A unit's 32 products and their sums are cut 23 bits below the largest term, which is
+    up to three times the terms' root mean square s: 34 cuts, each uniform over a step of
+    2^-23 * 3 s with either sign (0.58 of a step), against a sum of about sqrt(32) s:
+    sqrt(34) * 0.58 * 3 / sqrt(32) * 2^-23 = 1.8 * 2^-23. gate and up (each 1.8, and slopes
+    up to 1.2 of the activation: 2.8) and down (1.8) make 3.3 * 2^-23; x and h, split into two
+    f16 terms, add 2^-24 each, the f32 sums of the units and the activation's 4e-6 of the
+    few that cancel less than the rest: below 8 * 2^-23."""
+    f, bits, gs = FORMATS[fmt]
+    L = LR.Layer(m=m, hidden=512, inter=256, top_k=4, E=9, fmt=f, bits=bits, gs=gs, x_dtype=DT_F32, seed=90 + m)
+    got = build(L, out_dtype=DT_F32, path="decode")(*inputs(L)).cpu().double().numpy()
+    ref = L.reference(DT_F32)[0]
+    assert np.linalg.norm(got - ref) <= 2.0**-20 * np.linalg.norm(ref)
+
+
 def test_mlp_rows_do_not_mix():
     """A token with NaN and one with infinities leave the other tokens' results alone."""
     L = LR.Layer(m=6, hidden=256, inter=128, top_k=2, E=2, fmt=FMT_AFFINE, bits=4, gs=32, x_dtype=DT_BF16, seed=12)
