@@ -160,6 +160,11 @@ struct MlpArgs {
 bool mlp_few_supported(const MlpArgs &a);
 uint64_t mlp_few_workspace(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t S);
 cudaError_t launch_mlp_few(const MlpArgs &a, uint32_t *err, void *hf, cudaStream_t st);
+// The products for some tens of pairs an expert: ws holds the routing (ws_layout), own
+// the rest.
+bool mlp_mid_supported(const MlpArgs &a);
+uint64_t mlp_mid_workspace(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t S, uint32_t E);
+cudaError_t launch_mlp_mid(const MlpArgs &a, uint8_t *ws, uint8_t *own, cudaStream_t st);
 
 // moe_qmm_id's scalar validation (MOE_OK or the status moe_qmm_id would return).
 moe_status validate_call(const void *x, const uint32_t *ids, const void *packed, const void *scales,

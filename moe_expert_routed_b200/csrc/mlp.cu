@@ -37,7 +37,9 @@ bool layout(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t S, uint32_t E,
     L->z = L->h + al256(R * inter * (hd == MOE_F32 ? 4ull : 2ull));
     L->total = L->z + al256(R * hidden * 4ull);
     // the few-token kernels' planes of h take the same room
+    const uint64_t mid = mlp_mid_workspace(m, hidden, inter, S, E);
     if (L->total < L->h + al256(few)) L->total = L->h + al256(few);
+    if (L->total < L->h + al256(mid)) L->total = L->h + al256(mid);
     return true;
 }
 
@@ -100,6 +102,8 @@ moe_status moe_mlp(const void *x, const uint32_t *ids, const float *weights, con
     const bool few = path == MOE_PATH_DECODE || R <= 64u || R <= 4ull * num_experts;
     if (few && path != MOE_PATH_GROUPED && mlp_few_supported(a))
         return launch_mlp_few(a, (uint32_t *)ws, h, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    if (path == MOE_PATH_AUTO && mlp_mid_supported(a))
+        return launch_mlp_mid(a, ws, ws + L.h, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     const moe_dtype hd = h_dtype((int)x_dtype);
     LayerProduct layer{0u};
     v = run_product(x, ids, *gate_up, h, m, hidden, 2u * inter, n_expert_used, num_experts, x_dtype, hd, (int)act,

@@ -1,0 +1,468 @@
+// mlp_mid.cu -- the gated expert MLP for some tens of pairs an expert: a block of
+// tokens, a batch of sequences. Two grouped products on mma.sync over the routing's tiles
+// of up to 32 pairs,
+//   mid_product<UP>    h[p] = act(G_e x_t) * (U_e x_t)
+//   mid_product<DOWN>  z[p] = D_e h[p]
+// and the weighted sum of z.
+//
+// With so few columns a 128-row tcgen05 tile is bound by what hands it the dequantised
+// operand, stage by stage, not by its arithmetic; here codes go from shared memory to the
+// registers that the MMA reads. As in mlp_few.cu (operands and images are its own) the
+// codes stay exact f16 values and scales are applied to f32 sums of a unit of 32, so no
+// weight is rounded. Here all eight columns of an MMA are pairs: the four lanes of a row
+// take a quarter of the same unit each (of the same scale's 16 codes, NVFP4).
+//
+// A CTA: 256 weight rows, 32 a warp as two tiles, which share the registers of x. Per unit
+// and scheduler that is, for n blocks of 8 pairs, 32 n cycles of MMA beside about
+// 50 + 16 n instructions. Steps of 128 codes come by cp.async, RING - 1 ahead, one
+// barrier a step.
+#include "common.cuh"
+#include "internal.h"
+#include "mlp_codes.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr uint32_t MID_THREADS = 256, MID_WARPS = 8, MID_ROWS = 256, MID_BLOCKS = 4;
+constexpr uint32_t MID_PAIRS = 8 * MID_BLOCKS;  // of a tile
+
+// Bytes of a row's 128 codes in a stage: padded so that the lanes' quarters of eight rows
+// lie in different banks (3 bits: 14 words of 10 codes; 6 bits: two lanes can meet).
+__host__ __device__ constexpr uint32_t line(int m) {
+    return m == M_A8 ? 160u : m == M_A6 ? 112u : m == M_CB2 ? 48u : 80u;
+}
+// A pair's 128 values of x or h in a stage (read 16 bytes a lane; NVFP4 8).
+__host__ __device__ constexpr uint32_t x_line(int m) { return m == M_NV ? 288u : 320u; }
+__host__ __device__ constexpr uint32_t stage_bytes(int m) {
+    return MID_ROWS * line(m) + MID_PAIRS * (x_line(m) + 32u);
+}
+// Stages that leave room for two CTAs an SM.
+__host__ __device__ constexpr uint32_t ring(int m) { return 3u * stage_bytes(m) <= 112u * 1024u ? 3u : 2u; }
+constexpr uint32_t HB = 132;  // floats of a pair's 128 columns of h in the epilogue
+
+struct MidParams {
+    const uint8_t *w, *s, *a;    // packed codes, scales, affine biases or scale2 (or codebook)
+    const void *bias;            // expert biases, or null
+    const uint8_t *x;            // images: [token] (UP), [place among the sorted pairs] (DOWN)
+    const uint32_t *offsets, *sorted_pairs, *tiles, *tile_count;
+    void *out;                   // UP: images of h by sorted place; DOWN: z [pair][n] f32
+    uint32_t k, n, S;            // n: rows of out (UP: of gate, the up rows follow)
+    uint32_t row_bytes, groups, gshift;
+    int bias_dtype, act, order;  // order of h's values in its images
+};
+
+// Two f32 values in one 64-bit register pair.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// This lane's 8 codes of a unit from its row's line: quarter q, or (NVFP4) four of each
+// scale's 16; `code`: 3-bit codes before the quarter in the line.
+template <int MODE>
+__device__ __forceinline__ void quarter(uint32_t at, uint32_t u, uint32_t q, uint32_t code, uint32_t (&w)[words(MODE)]) {
+    if constexpr (MODE == M_NV) {
+        w[0] = lds16(at + u * 16u + q * 2u) | lds16(at + u * 16u + 8u + q * 2u) << 16;
+    } else if constexpr (MODE == M_A8) {
+        const uint2 v = lds64(at + u * 32u + q * 8u);
+        w[0] = v.x; w[1] = v.y;
+    } else if constexpr (MODE == M_A6) {
+        const uint32_t p = at + u * 24u + q * 6u;
+        w[0] = lds16(p) | lds16(p + 2u) << 16;
+        w[1] = lds16(p + 4u);
+    } else if constexpr (MODE == M_CB2) {
+        w[0] = lds16(at + u * 8u + q * 2u);
+    } else if constexpr (MODE == M_CB3) {
+        const uint32_t word = code * 205u >> 11, m = 0x3FFFFFFFu;  // code / 10 (codes below 138)
+        const uint32_t a = lds32(at + word * 4u) & m, b = lds32(at + word * 4u + 4u) & m;
+        w[0] = __funnelshift_r(a | (b << 30), b >> 2, 3u * (code - 10u * word));
+    } else {
+        w[0] = lds32(at + u * 16u + q * 4u);
+    }
+}
+
+// A unit's scale as it is stored (NVFP4: two), and as f32; affine codes are f16 integers
+// times 2^-24.
+template <int MODE>
+__device__ __forceinline__ uint32_t raw_scale(const uint8_t *p) {
+    if constexpr (MODE == M_MX) return __ldg(p);
+    else return __ldg((const uint16_t *)p);
+}
+template <int MODE>
+__device__ __forceinline__ float scale_f32(uint32_t v) {
+    if constexpr (affine(MODE)) return bf16_bits_to_f32(v) * 16777216.f;
+    else if constexpr (codebook(MODE)) return f16_bits_to_f32(v);
+    else return e8m0_to_f32(v);
+}
+
+// The warp's 32 rows x `units` units of a step x 8 NT pairs. A row: shared address of the
+// lane's first row, xs, fs: of its part of the pairs' values and (factor, sum)s; c0: 3-bit codes
+// before the step in the line; raw, rawb: unit q's scales of the lane's four rows.
+template <int MODE, int NT>
+__device__ __forceinline__ void mid_step(uint32_t row, uint32_t xs, uint32_t fs, uint32_t units, uint32_t c0,
+                                         const uint32_t (&raw)[4], const uint32_t (&rawb)[4], const Table<MODE> &tab,
+                                         uint32_t lane, uint64_t (&acc)[2][2][MID_BLOCKS]) {
+    const uint32_t q = lane & 3u;
+#pragma unroll
+    for (uint32_t u = 0; u < 4; u++) {
+        if (u >= units) break;
+        uint32_t p[4][4];
+        uint64_t s[4], s1[MODE == M_NV ? 4 : 1], b[affine(MODE) ? 4 : 1];
+#pragma unroll
+        for (uint32_t i = 0; i < 4; i++) {
+            uint32_t w[words(MODE)];
+            quarter<MODE>(row + 8u * i * line(MODE), u, q, c0 + 32u * u + 8u * q, w);
+            expand<MODE, false>(w, 0, tab, p[i]);
+            const uint32_t v = __shfl_sync(FULL, raw[i], (lane & ~3u) | u);
+            if constexpr (MODE == M_NV) {
+                float f0, f1;
+                from_e4m3x2(v, f0, f1);
+                s[i] = pack2(f0, f0);
+                s1[i] = pack2(f1, f1);
+            } else {
+                const float f = scale_f32<MODE>(v);
+                s[i] = pack2(f, f);
+            }
+            if constexpr (affine(MODE)) {
+                const float f = bf16_bits_to_f32(__shfl_sync(FULL, rawb[i], (lane & ~3u) | u));
+                b[i] = pack2(f, f);
+            }
+        }
+#pragma unroll
+        for (uint32_t n = 0; n < NT; n++) {
+            uint4 B;
+            if constexpr (MODE == M_NV) {
+                const uint2 lo = lds64(xs + n * 8u * x_line(MODE) + u * 64u);
+                const uint2 hi = lds64(xs + n * 8u * x_line(MODE) + u * 64u + 32u);
+                B = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            } else {
+                B = lds128(xs + n * 8u * x_line(MODE) + u * 64u);
+            }
+            const uint4 F = lds128(fs + (u * MID_PAIRS + n * 8u) * 8u);
+            const uint64_t f = pack2(__uint_as_float(F.x), __uint_as_float(F.z));
+            const uint64_t sum = pack2(__uint_as_float(F.y), __uint_as_float(F.w));
+#pragma unroll
+            for (uint32_t t = 0; t < 2; t++) {
+                const uint32_t i = 2u * t;
+                float c[4], d[4];
+                mma0(c, p[i][0], p[i + 1][0], p[i][1], p[i + 1][1], B.x, B.y);
+                if constexpr (MODE == M_NV) mma0(d, p[i][2], p[i + 1][2], p[i][3], p[i + 1][3], B.z, B.w);
+                else mma(c, p[i][2], p[i + 1][2], p[i][3], p[i + 1][3], B.z, B.w);
+#pragma unroll
+                for (uint32_t h = 0; h < 2; h++) {
+                    uint64_t &to = acc[t][h][n];
+                    const uint64_t c2 = pack2(c[2 * h], c[2 * h + 1]);
+                    if constexpr (MODE == M_NV)
+                        to = fma2(f, fma2(s1[i + h], pack2(d[2 * h], d[2 * h + 1]), mul2(s[i + h], c2)), to);
+                    else
+                        to = fma2(s[i + h], mul2(f, c2), to);
+                    if constexpr (affine(MODE)) to = fma2(b[i + h], sum, to);
+                }
+            }
+        }
+    }
+}
+
+// grid (blocks of 256 rows, tiles).
+template <int MODE, bool UP>
+__global__ void __launch_bounds__(MID_THREADS, 2) mid_product(const MidParams P) {
+    constexpr uint32_t LINE = line(MODE), XL = x_line(MODE), STAGE = stage_bytes(MODE), RINGS = ring(MODE);
+    constexpr uint32_t X_AT = MID_ROWS * LINE, F_AT = X_AT + MID_PAIRS * XL;
+    static_assert(MID_PAIRS * HB * 4u <= RINGS * STAGE, "the epilogue's h takes the ring's room");
+    extern __shared__ __align__(16) uint8_t sm[];
+    if (blockIdx.y >= __ldg(P.tile_count)) return;
+    const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u, r = lane >> 2, q = lane & 3u;
+    const uint32_t e = __ldg(P.tiles + 2u * blockIdx.y), r0 = __ldg(P.tiles + 2u * blockIdx.y + 1u);
+    const uint32_t place = __ldg(P.offsets + e) + r0;
+    const uint32_t np = tmin<uint32_t>(__ldg(P.offsets + e + 1u) - place, MID_PAIRS), nt = (np + 7u) / 8u;
+    const uint32_t nu = P.k / 32u, steps = (nu + 3u) / 4u, srow = scale_bytes(MODE, P.groups);
+
+    // the lane's rows r, r + 8 of two tiles; UP: gate and up of 8 columns are a tile
+    const uint32_t row0 = blockIdx.x * (UP ? 128u : 256u) + warp * (UP ? 16u : 32u);
+    const bool active = row0 < P.n;
+    const size_t first = (size_t)e * (UP ? 2u : 1u) * P.n + (active ? row0 : 0u) + r;
+    const size_t dr = UP ? P.n : 8u, dt = UP ? 8u : 16u;  // rows on to the lane's second, and to the next tile
+    const uint8_t *const w0 = P.w + first * P.row_bytes, *const s0 = P.s + first * srow, *const b0 = P.a + first * srow;
+    const uint32_t sm0 = ptx::smem_u32(sm);
+
+    // this warp's pairs: warp, warp + 8, ...
+    const uint8_t *src[MID_BLOCKS];
+#pragma unroll
+    for (uint32_t i = 0; i < MID_BLOCKS; i++) {
+        const uint32_t pr = warp + 8u * i;
+        const uint32_t at = place + (pr < np ? pr : 0u);
+        const size_t img = UP ? __ldg(P.sorted_pairs + at) / P.S : at;
+        src[i] = P.x + img * steps * step_bytes(1);
+    }
+    auto issue = [&](uint32_t j, uint32_t slot) {
+        if (j < steps) {
+            const uint32_t st = sm0 + slot * STAGE;
+            if (active) {
+#pragma unroll
+                for (uint32_t i = 0; i < 4; i++) {
+                    const uint8_t *g = w0 + ((i & 1u) * dr + (i >> 1) * dt) * P.row_bytes;
+                    const uint32_t d = st + (warp * 32u + 8u * i + r) * LINE;
+                    if constexpr (MODE == M_CB3) {
+                        const uint32_t word = 128u * j / 10u + q;
+#pragma unroll
+                        for (uint32_t k = 0; k < 16; k += 4)
+                            if (k < 12u || q < 2u)  // 14 words
+                                ptx::cp_async_4(d + (q + k) * 4u, g + (word + k < P.row_bytes / 4u ? (word + k) * 4u : 0u),
+                                                word + k < P.row_bytes / 4u ? 4u : 0u);
+                    } else if constexpr (MODE == M_CB2) {
+                        const uint32_t in = 4u * j + q < nu;
+                        ptx::cp_async_8(d + q * 8u, g + (in ? (4u * j + q) * 8u : 0u), in ? 8u : 0u);
+                    } else if constexpr (MODE == M_A6) {
+#pragma unroll
+                        for (uint32_t k = 0; k < 3; k++) {
+                            const uint32_t o = (q + 4u * k) * 8u, in = 96u * j + o < P.row_bytes;
+                            ptx::cp_async_8(d + o, g + (in ? 96u * j + o : 0u), in ? 8u : 0u);
+                        }
+                    } else {
+                        constexpr uint32_t STEP = MODE == M_A8 ? 128u : 64u;
+#pragma unroll
+                        for (uint32_t k = 0; k < STEP / 64u; k++) {
+                            const uint32_t o = (q + 4u * k) * 16u, in = STEP * j + o < P.row_bytes;
+                            ptx::cp_async_16(d + o, g + (in ? STEP * j + o : 0u), in ? 16u : 0u);
+                        }
+                    }
+                }
+            }
+            // the pairs' images: values by pair, (factor, sum) by unit and pair
+#pragma unroll
+            for (uint32_t i = 0; i < MID_BLOCKS; i++) {
+                const uint32_t pr = warp + 8u * i;
+                if (pr < np) {
+                    const uint8_t *g = src[i] + j * step_bytes(1);
+                    if (lane < 16u) ptx::cp_async_16(st + X_AT + pr * XL + lane * 16u, g + lane * 16u, 16u);
+                    else if (lane < 20u)
+                        ptx::cp_async_8(st + F_AT + ((lane - 16u) * MID_PAIRS + pr) * 8u, g + 256u + (lane - 16u) * 8u, 8u);
+                }
+            }
+        }
+        ptx::cp_async_commit();
+    };
+    // scales of unit q of a step, a step ahead, in registers
+    uint32_t raw[4], rawb[4] = {0u, 0u, 0u, 0u}, nraw[4], nrawb[4] = {0u, 0u, 0u, 0u};
+    auto fetch = [&](uint32_t j) {
+        const uint32_t o = scale_entry<MODE>(tmin<uint32_t>(4u * j + q, nu - 1u), P.gshift);
+#pragma unroll
+        for (uint32_t i = 0; i < 4; i++) {
+            const size_t row = ((i & 1u) * dr + (i >> 1) * dt) * srow;
+            nraw[i] = raw_scale<MODE>(s0 + row + o);
+            if constexpr (affine(MODE)) nrawb[i] = raw_scale<MODE>(b0 + row + o);
+        }
+    };
+    for (uint32_t i = 0; i + 1u < RINGS; i++) issue(i, i);
+    fetch(0u);
+    Table<MODE> tab;
+    tab.load(P.a);
+
+    uint64_t acc[2][2][MID_BLOCKS];
+#pragma unroll
+    for (uint32_t t = 0; t < 4; t++)
+#pragma unroll
+        for (uint32_t n = 0; n < MID_BLOCKS; n++) acc[t >> 1][t & 1][n] = 0ull;
+
+    const uint32_t row = sm0 + (warp * 32u + r) * LINE, xs = sm0 + X_AT + r * XL + q * (MODE == M_NV ? 8u : 16u),
+                   fs = sm0 + F_AT + q * 16u;
+    uint32_t slot = 0;
+    for (uint32_t j = 0; j < steps; j++) {
+        wait_groups<(int)RINGS - 2>();
+        __syncthreads();  // the step has landed, and the slot of the step before is free
+        issue(j + RINGS - 1u, slot == 0u ? RINGS - 1u : slot - 1u);
+#pragma unroll
+        for (uint32_t i = 0; i < 4; i++) raw[i] = nraw[i], rawb[i] = nrawb[i];
+        if (j + 1u < steps) fetch(j + 1u);
+        if (active) {
+            const uint32_t on = slot * STAGE, units = tmin<uint32_t>(nu - 4u * j, 4u);
+            const uint32_t c0 = MODE == M_CB3 ? 128u * j % 10u : 0u;
+            switch (nt) {
+                case 1: mid_step<MODE, 1>(row + on, xs + on, fs + on, units, c0, raw, rawb, tab, lane, acc); break;
+                case 2: mid_step<MODE, 2>(row + on, xs + on, fs + on, units, c0, raw, rawb, tab, lane, acc); break;
+                case 3: mid_step<MODE, 3>(row + on, xs + on, fs + on, units, c0, raw, rawb, tab, lane, acc); break;
+                default: mid_step<MODE, 4>(row + on, xs + on, fs + on, units, c0, raw, rawb, tab, lane, acc);
+            }
+        }
+        slot = slot + 1u == RINGS ? 0u : slot + 1u;
+    }
+    wait_groups<0>();
+
+    const float s2 = MODE == M_NV ? __ldg((const float *)P.a + e) : 1.f;
+    if constexpr (!UP) {
+        if (!active) return;
+        float *const z = (float *)P.out;
+        float bias[4];
+#pragma unroll
+        for (uint32_t i = 0; i < 4; i++)
+            bias[i] = load_bias(P.bias, P.bias_dtype, (size_t)e * P.n + row0 + 8u * i + r);
+#pragma unroll
+        for (uint32_t n = 0; n < MID_BLOCKS; n++)
+#pragma unroll
+            for (uint32_t k = 0; k < 2; k++) {
+                const uint32_t pr = 8u * n + 2u * q + k;
+                if (pr < np) {
+                    float *const to = z + (size_t)__ldg(P.sorted_pairs + place + pr) * P.n + row0 + r;
+#pragma unroll
+                    for (uint32_t i = 0; i < 4; i++) {
+                        const float2 v = unpack2(acc[i >> 1][i & 1][n]);
+                        to[8u * i] = fmaf(k ? v.y : v.x, s2, bias[i]);
+                    }
+                }
+            }
+    } else {
+        __syncthreads();  // every warp has left the ring
+        float *const hb = (float *)sm;
+        if (active) {
+#pragma unroll
+            for (uint32_t t = 0; t < 2; t++) {
+                const uint32_t c = warp * 16u + 8u * t + r;
+                const size_t bo = (size_t)e * 2u * P.n + row0 + 8u * t + r;
+                const float bg = load_bias(P.bias, P.bias_dtype, bo), bu = load_bias(P.bias, P.bias_dtype, bo + P.n);
+#pragma unroll
+                for (uint32_t n = 0; n < MID_BLOCKS; n++) {
+                    const float2 g = unpack2(acc[t][0][n]), u = unpack2(acc[t][1][n]);
+                    const uint32_t pr = 8u * n + 2u * q;
+                    if (pr < np) hb[pr * HB + c] = glu_act(P.act, fmaf(g.x, s2, bg)) * fmaf(u.x, s2, bu);
+                    if (pr + 1u < np) hb[(pr + 1u) * HB + c] = glu_act(P.act, fmaf(g.y, s2, bg)) * fmaf(u.y, s2, bu);
+                }
+            }
+        }
+        __syncthreads();
+        // a warp writes a unit of 32 columns of a pair: one step's images, 4 units, a CTA
+        const uint32_t units = tmin<uint32_t>((P.n - blockIdx.x * 128u) / 32u, 4u), hsteps = (P.n + 127u) / 128u;
+        for (uint32_t o = warp; o < 4u * np; o += MID_WARPS) {
+            const uint32_t pr = o >> 2, un = o & 3u;
+            if (un >= units) continue;  // past the last column: no unit there is read
+            float h = hb[pr * HB + un * 32u + lane], sum = h;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(FULL, sum, d);
+            float scale, factor;
+            unit_scale(__reduce_max_sync(FULL, __float_as_uint(h) & 0x7FFFFFFFu), scale, factor);
+            h *= scale;
+            if (P.order == 1 && (lane & 1u)) h *= 0.0625f;  // meets a 16-fold pair
+            uint8_t *img = (uint8_t *)P.out + ((size_t)(place + pr) * hsteps + blockIdx.x) * step_bytes(1);
+            ((uint16_t *)(img + un * 64u))[b_place(P.order, lane)] = __half_as_ushort(__float2half_rn(h));
+            if (lane == 0) ((float2 *)(img + 256u))[un] = make_float2(factor, sum);
+        }
+    }
+}
+
+// The tokens' images, in the order of MODE's codes. grid (tokens, blocks of 8 steps).
+template <int MODE>
+__global__ void __launch_bounds__(MID_THREADS) mid_images(const void *x, int dt, uint32_t k, uint8_t *img) {
+    const uint32_t lane = threadIdx.x & 31u, j = blockIdx.y * MID_WARPS + (threadIdx.x >> 5), c = j * 128u + 4u * lane;
+    const uint32_t steps = (k + 127u) / 128u;
+    if (j >= steps) return;
+    const float4 v = c < k ? load_x4(x, dt, (size_t)blockIdx.x * k + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    write_step<MODE, 1>(img + ((size_t)blockIdx.x * steps + j) * step_bytes(1), v, lane);
+}
+
+template <int MODE, bool UP>
+cudaError_t product(const MidParams &P, uint32_t max_tiles, cudaStream_t st) {
+    auto kern = mid_product<MODE, UP>;
+    const size_t smem = (size_t)ring(MODE) * stage_bytes(MODE);
+    static int smem_set[64];
+    const cudaError_t e = ensure_dyn_smem(kern, smem, smem_set);
+    if (e != cudaSuccess) return e;
+    kern<<<dim3((P.n * (UP ? 2u : 1u) + MID_ROWS - 1u) / MID_ROWS, max_tiles), MID_THREADS, smem, st>>>(P);
+    return cudaGetLastError();
+}
+
+template <bool UP>
+cudaError_t product_m(const MidParams &P, int mode, uint32_t max_tiles, cudaStream_t st) {
+    switch (mode) {
+        case M_A4:
+        case M_A4U: return product<M_A4U, UP>(P, max_tiles, st);
+        case M_A6: return product<M_A6, UP>(P, max_tiles, st);
+        case M_A8: return product<M_A8, UP>(P, max_tiles, st);
+        case M_NV: return product<M_NV, UP>(P, max_tiles, st);
+        case M_MX: return product<M_MX, UP>(P, max_tiles, st);
+        case M_CB2: return product<M_CB2, UP>(P, max_tiles, st);
+        case M_CB3: return product<M_CB3, UP>(P, max_tiles, st);
+        default: return product<M_CB4, UP>(P, max_tiles, st);
+    }
+}
+
+inline uint64_t al256(uint64_t v) { return (v + 255u) & ~255ull; }
+uint64_t images(uint64_t rows, uint32_t k) { return al256(rows * ((k + 127ull) / 128ull) * step_bytes(1)); }
+uint32_t tiles_of(uint64_t R, uint32_t E) { return (uint32_t)(R / MID_PAIRS) + E + 1u; }
+
+}  // namespace
+
+// Pairs of up to MOE_MLP_MID_PAIRS an expert.
+static uint64_t mid_limit(uint32_t E) { return tmin<uint64_t>((uint64_t)MOE_MLP_MID_PAIRS * E, 1u << 20); }
+
+uint64_t mlp_mid_workspace(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t S, uint32_t E) {
+    // with more pairs than it takes, what fewer pairs in the same workspace need
+    const uint64_t R = tmin<uint64_t>((uint64_t)m * S, mid_limit(E)), tokens = tmin<uint64_t>(m, R);
+    return al256(8ull * tiles_of(R, E)) + images(tokens, hidden) + images(R, inter) + R * hidden * 4ull;
+}
+
+bool mlp_mid_supported(const MlpArgs &a) {
+    const uint64_t R = (uint64_t)a.m * a.S;
+    return R <= mid_limit(a.E) && a.E <= MOE_ROUTE_MAX_EXPERTS && a.x_dtype != DT_F32 && a.out_dtype != DT_F32 &&
+           mode_of(*a.gate_up, a.hidden) >= 0 && mode_of(*a.down, a.inter) >= 0 && ((uintptr_t)a.x & 7u) == 0;
+}
+
+cudaError_t launch_mlp_mid(const MlpArgs &a, uint8_t *ws, uint8_t *own, cudaStream_t st) {
+    const uint32_t R = a.m * a.S, max_tiles = tiles_of(R, a.E);
+    WsLayout L;
+    if (!ws_layout(R, a.E, &L)) return cudaErrorInvalidValue;
+    uint32_t *const err = (uint32_t *)(ws + L.err), *const tc = (uint32_t *)(ws + L.tile_count);
+    uint32_t *const counts = (uint32_t *)(ws + L.counts), *const offsets = (uint32_t *)(ws + L.offsets);
+    uint32_t *const sp = (uint32_t *)(ws + L.sorted_pairs), *const tiles = (uint32_t *)own;
+    uint8_t *const xi = own + al256(8ull * max_tiles), *const hi = xi + images(a.m, a.hidden);
+    float *const z = (float *)(hi + images(R, a.inter));
+    cudaError_t e = launch_route(a.ids, R, a.E, MID_PAIRS, counts, offsets, sp, tiles, tc, max_tiles,
+                                 (uint32_t *)(ws + L.chunk_hist), (uint32_t *)(ws + L.chunk_base), L.chunks, err, nullptr,
+                                 0, 0, st);
+    if (e != cudaSuccess) return e;
+    const int m1 = mode_of(*a.gate_up, a.hidden), m2 = mode_of(*a.down, a.inter);
+    const dim3 grid(a.m, ((a.hidden + 127u) / 128u + MID_WARPS - 1u) / MID_WARPS);
+    if (order_of(m1) == 1) mid_images<M_A4><<<grid, MID_THREADS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi);
+    else if (order_of(m1) == 2) mid_images<M_A8><<<grid, MID_THREADS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi);
+    else if (m1 == M_A6) mid_images<M_A6><<<grid, MID_THREADS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi);
+    else mid_images<M_NV><<<grid, MID_THREADS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+
+    MidParams P{};
+    P.w = (const uint8_t *)a.gate_up->packed; P.s = (const uint8_t *)a.gate_up->scales;
+    P.a = (const uint8_t *)a.gate_up->aux; P.bias = a.gate_up->bias; P.bias_dtype = (int)a.gate_up->bias_dtype;
+    P.x = xi; P.out = hi;
+    P.offsets = offsets; P.sorted_pairs = sp; P.tiles = tiles; P.tile_count = tc;
+    P.k = a.hidden; P.n = a.inter; P.S = a.S;
+    P.row_bytes = (uint32_t)moe_packed_row_bytes(a.gate_up->fmt, a.gate_up->bits, a.hidden);
+    P.groups = a.hidden / a.gate_up->group_size; P.gshift = log2_units(*a.gate_up);
+    P.act = a.act; P.order = order_of(m2);
+    e = product_m<true>(P, m1, max_tiles, st);
+    if (e != cudaSuccess) return e;
+    P.w = (const uint8_t *)a.down->packed; P.s = (const uint8_t *)a.down->scales;
+    P.a = (const uint8_t *)a.down->aux; P.bias = a.down->bias; P.bias_dtype = (int)a.down->bias_dtype;
+    P.x = hi; P.out = z;
+    P.k = a.inter; P.n = a.hidden;
+    P.row_bytes = (uint32_t)moe_packed_row_bytes(a.down->fmt, a.down->bits, a.inter);
+    P.groups = a.inter / a.down->group_size; P.gshift = log2_units(*a.down);
+    e = product_m<false>(P, m2, max_tiles, st);
+    if (e != cudaSuccess) return e;
+    return launch_combine(z, a.weights, a.ids, a.residual, a.out, a.m, a.S, a.hidden, a.E, DT_F32, a.out_dtype, st);
+}
+
+}  // namespace moe
