@@ -28,7 +28,7 @@ constexpr uint32_t MID_THREADS = 256, MID_WARPS = 8, MID_ROWS = 256, MID_BLOCKS 
 constexpr uint32_t MID_PAIRS = 8 * MID_BLOCKS;  // of a tile
 
 // Bytes of a row's 128 codes in a stage: padded so that the lanes' quarters of eight rows
-// lie in different banks (3 bits: 14 words of 10 codes; 6 bits: two lanes can meet).
+// lie in different banks (3 bits: the 16-byte blocks that hold 14 words of 10 codes; 6 bits: two lanes can meet).
 __host__ __device__ constexpr uint32_t line(int m) {
     return m == M_A8 ? 160u : m == M_A6 ? 112u : m == M_CB2 ? 48u : 80u;
 }
@@ -102,8 +102,11 @@ __device__ __forceinline__ void quarter(uint32_t at, uint32_t u, uint32_t q, uin
 // times 2^-24.
 template <int MODE>
 __device__ __forceinline__ uint32_t raw_scale(const uint8_t *p) {
-    if constexpr (MODE == M_MX) return __ldg(p);
-    else return __ldg((const uint16_t *)p);
+    // volatile: requested where it stands, a step ahead of its use
+    uint16_t v;
+    if constexpr (MODE == M_MX) asm volatile("{.reg .u8 b; ld.global.nc.u8 b, [%1]; cvt.u16.u8 %0, b;}" : "=h"(v) : "l"(p));
+    else asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
 }
 template <int MODE>
 __device__ __forceinline__ float scale_f32(uint32_t v) {
@@ -112,17 +115,16 @@ __device__ __forceinline__ float scale_f32(uint32_t v) {
     else return e8m0_to_f32(v);
 }
 
-// The warp's 32 rows x `units` units of a step x 8 NT pairs. A row: shared address of the
+// The warp's 32 rows x a step x 8 NT pairs; past the last column codes and x are zero. row: shared address of the
 // lane's first row, xs, fs: of its part of the pairs' values and (factor, sum)s; c0: 3-bit codes
 // before the step in the line; raw, rawb: unit q's scales of the lane's four rows.
 template <int MODE, int NT>
-__device__ __forceinline__ void mid_step(uint32_t row, uint32_t xs, uint32_t fs, uint32_t units, uint32_t c0,
+__device__ __forceinline__ void mid_step(uint32_t row, uint32_t xs, uint32_t fs, uint32_t c0,
                                          const uint32_t (&raw)[4], const uint32_t (&rawb)[4], const Table<MODE> &tab,
                                          uint32_t lane, uint64_t (&acc)[2][2][MID_BLOCKS]) {
     const uint32_t q = lane & 3u;
 #pragma unroll
     for (uint32_t u = 0; u < 4; u++) {
-        if (u >= units) break;
         uint32_t p[4][4];
         uint64_t s[4], s1[MODE == M_NV ? 4 : 1], b[affine(MODE) ? 4 : 1];
 #pragma unroll
@@ -202,15 +204,18 @@ __global__ void __launch_bounds__(MID_THREADS, 2) mid_product(const MidParams P)
     const uint8_t *const w0 = P.w + first * P.row_bytes, *const s0 = P.s + first * srow, *const b0 = P.a + first * srow;
     const uint32_t sm0 = ptx::smem_u32(sm);
 
-    // this warp's pairs: warp, warp + 8, ...
-    const uint8_t *src[MID_BLOCKS];
-#pragma unroll
-    for (uint32_t i = 0; i < MID_BLOCKS; i++) {
-        const uint32_t pr = warp + 8u * i;
+    // half a warp copies a pair's values, a quad the (factor, sum)s of a pair's four units
+    auto image = [&](uint32_t pr) {
         const uint32_t at = place + (pr < np ? pr : 0u);
         const size_t img = UP ? __ldg(P.sorted_pairs + at) / P.S : at;
-        src[i] = P.x + img * steps * step_bytes(1);
-    }
+        return P.x + img * steps * step_bytes(1);
+    };
+    const uint32_t vp = 2u * warp + (lane >> 4), fp = 8u * warp + r;  // and vp + 16
+    const uint8_t *const v0 = image(vp) + (lane & 15u) * 16u, *const v1 = image(vp + 16u) + (lane & 15u) * 16u;
+    const uint8_t *const f0 = image(fp) + 256u + q * 8u;
+    const uint32_t vd = X_AT + vp * XL + (lane & 15u) * 16u, fd = F_AT + (q * MID_PAIRS + fp) * 8u;
+    // 3-bit codes: the 16-byte blocks of memory that hold a step's 14 words
+    const uint32_t rw = P.row_bytes / 4u, misplaced = MODE == M_CB3 ? r * rw : 0u;
     auto issue = [&](uint32_t j, uint32_t slot) {
         if (j < steps) {
             const uint32_t st = sm0 + slot * STAGE;
@@ -220,12 +225,13 @@ __global__ void __launch_bounds__(MID_THREADS, 2) mid_product(const MidParams P)
                     const uint8_t *g = w0 + ((i & 1u) * dr + (i >> 1) * dt) * P.row_bytes;
                     const uint32_t d = st + (warp * 32u + 8u * i + r) * LINE;
                     if constexpr (MODE == M_CB3) {
-                        const uint32_t word = 128u * j / 10u + q;
-#pragma unroll
-                        for (uint32_t k = 0; k < 16; k += 4)
-                            if (k < 12u || q < 2u)  // 14 words
-                                ptx::cp_async_4(d + (q + k) * 4u, g + (word + k < P.row_bytes / 4u ? (word + k) * 4u : 0u),
-                                                word + k < P.row_bytes / 4u ? 4u : 0u);
+                        const int word = (int)(128u * j / 10u), off = (int)(misplaced + word) & 3;
+                        auto block = [&](uint32_t k) {  // up to the row's end
+                            const int o = (word - off) * 4 + (int)k * 16, n = (int)P.row_bytes - o;
+                            ptx::cp_async_16(d + k * 16u, g + (n > 0 ? o : 0), n >= 16 ? 16u : n > 0 ? (uint32_t)n : 0u);
+                        };
+                        block(q);
+                        if (off == 3 && q == i) block(4u);  // 14 words from a block's fourth on: a fifth block
                     } else if constexpr (MODE == M_CB2) {
                         const uint32_t in = 4u * j + q < nu;
                         ptx::cp_async_8(d + q * 8u, g + (in ? (4u * j + q) * 8u : 0u), in ? 8u : 0u);
@@ -245,17 +251,10 @@ __global__ void __launch_bounds__(MID_THREADS, 2) mid_product(const MidParams P)
                     }
                 }
             }
-            // the pairs' images: values by pair, (factor, sum) by unit and pair
-#pragma unroll
-            for (uint32_t i = 0; i < MID_BLOCKS; i++) {
-                const uint32_t pr = warp + 8u * i;
-                if (pr < np) {
-                    const uint8_t *g = src[i] + j * step_bytes(1);
-                    if (lane < 16u) ptx::cp_async_16(st + X_AT + pr * XL + lane * 16u, g + lane * 16u, 16u);
-                    else if (lane < 20u)
-                        ptx::cp_async_8(st + F_AT + ((lane - 16u) * MID_PAIRS + pr) * 8u, g + 256u + (lane - 16u) * 8u, 8u);
-                }
-            }
+            const uint32_t o = j * step_bytes(1);
+            ptx::cp_async_16_if(vp < np, st + vd, v0 + o, 16u);
+            ptx::cp_async_16_if(vp + 16u < np, st + vd + 16u * XL, v1 + o, 16u);
+            if (fp < np) ptx::cp_async_8(st + fd, f0 + o, 8u);
         }
         ptx::cp_async_commit();
     };
@@ -292,13 +291,13 @@ __global__ void __launch_bounds__(MID_THREADS, 2) mid_product(const MidParams P)
         for (uint32_t i = 0; i < 4; i++) raw[i] = nraw[i], rawb[i] = nrawb[i];
         if (j + 1u < steps) fetch(j + 1u);
         if (active) {
-            const uint32_t on = slot * STAGE, units = tmin<uint32_t>(nu - 4u * j, 4u);
-            const uint32_t c0 = MODE == M_CB3 ? 128u * j % 10u : 0u;
+            const uint32_t on = slot * STAGE;
+            const uint32_t c0 = MODE == M_CB3 ? 128u * j % 10u : 0u, o = MODE == M_CB3 ? (misplaced + 128u * j / 10u) % 4u * 4u : 0u;
             switch (nt) {
-                case 1: mid_step<MODE, 1>(row + on, xs + on, fs + on, units, c0, raw, rawb, tab, lane, acc); break;
-                case 2: mid_step<MODE, 2>(row + on, xs + on, fs + on, units, c0, raw, rawb, tab, lane, acc); break;
-                case 3: mid_step<MODE, 3>(row + on, xs + on, fs + on, units, c0, raw, rawb, tab, lane, acc); break;
-                default: mid_step<MODE, 4>(row + on, xs + on, fs + on, units, c0, raw, rawb, tab, lane, acc);
+                case 1: mid_step<MODE, 1>(row + on + o, xs + on, fs + on, c0, raw, rawb, tab, lane, acc); break;
+                case 2: mid_step<MODE, 2>(row + on + o, xs + on, fs + on, c0, raw, rawb, tab, lane, acc); break;
+                case 3: mid_step<MODE, 3>(row + on + o, xs + on, fs + on, c0, raw, rawb, tab, lane, acc); break;
+                default: mid_step<MODE, 4>(row + on + o, xs + on, fs + on, c0, raw, rawb, tab, lane, acc);
             }
         }
         slot = slot + 1u == RINGS ? 0u : slot + 1u;
@@ -350,8 +349,7 @@ __global__ void __launch_bounds__(MID_THREADS, 2) mid_product(const MidParams P)
         const uint32_t units = tmin<uint32_t>((P.n - blockIdx.x * 128u) / 32u, 4u), hsteps = (P.n + 127u) / 128u;
         for (uint32_t o = warp; o < 4u * np; o += MID_WARPS) {
             const uint32_t pr = o >> 2, un = o & 3u;
-            if (un >= units) continue;  // past the last column: no unit there is read
-            float h = hb[pr * HB + un * 32u + lane], sum = h;
+            float h = un < units ? hb[pr * HB + un * 32u + lane] : 0.f, sum = h;  // zeros past the last column
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(FULL, sum, d);
             float scale, factor;
