@@ -103,9 +103,9 @@ __device__ __forceinline__ void quarter(uint32_t at, uint32_t u, uint32_t q, uin
 template <int MODE>
 __device__ __forceinline__ uint32_t raw_scale(const uint8_t *p) {
     // volatile: requested where it stands, a step ahead of its use
-    uint16_t v;
-    if constexpr (MODE == M_MX) asm volatile("{.reg .u8 b; ld.global.nc.u8 b, [%1]; cvt.u16.u8 %0, b;}" : "=h"(v) : "l"(p));
-    else asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    uint32_t v;
+    if constexpr (MODE == M_MX) asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(p));
+    else asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(v) : "l"(p));
     return v;
 }
 template <int MODE>
@@ -117,22 +117,29 @@ __device__ __forceinline__ float scale_f32(uint32_t v) {
 
 // The warp's 32 rows x a step x 8 NT pairs; past the last column codes and x are zero. row: shared address of the
 // lane's first row, xs, fs: of its part of the pairs' values and (factor, sum)s; c0: 3-bit codes
-// before the step in the line; raw, rawb: unit q's scales of the lane's four rows.
+// before the step in the line; raw, rawb: unit q's scales of the lane's four
+// rows, two in a register.
 template <int MODE, int NT>
 __device__ __forceinline__ void mid_step(uint32_t row, uint32_t xs, uint32_t fs, uint32_t c0,
-                                         const uint32_t (&raw)[4], const uint32_t (&rawb)[4], const Table<MODE> &tab,
+                                         const uint32_t (&raw)[2], const uint32_t (&rawb)[2], const Table<MODE> &tab,
                                          uint32_t lane, uint64_t (&acc)[2][2][MID_BLOCKS]) {
     const uint32_t q = lane & 3u;
 #pragma unroll
     for (uint32_t u = 0; u < 4; u++) {
         uint32_t p[4][4];
         uint64_t s[4], s1[MODE == M_NV ? 4 : 1], b[affine(MODE) ? 4 : 1];
+        uint32_t sv[2], bv[2];
+#pragma unroll
+        for (uint32_t t = 0; t < 2; t++) {
+            sv[t] = __shfl_sync(FULL, raw[t], (lane & ~3u) | u);
+            if constexpr (affine(MODE)) bv[t] = __shfl_sync(FULL, rawb[t], (lane & ~3u) | u);
+        }
 #pragma unroll
         for (uint32_t i = 0; i < 4; i++) {
             uint32_t w[words(MODE)];
             quarter<MODE>(row + 8u * i * line(MODE), u, q, c0 + 32u * u + 8u * q, w);
             expand<MODE, false>(w, 0, tab, p[i]);
-            const uint32_t v = __shfl_sync(FULL, raw[i], (lane & ~3u) | u);
+            const uint32_t v = i & 1u ? sv[i >> 1] >> 16 : sv[i >> 1] & 0xFFFFu;
             if constexpr (MODE == M_NV) {
                 float f0, f1;
                 from_e4m3x2(v, f0, f1);
@@ -143,7 +150,7 @@ __device__ __forceinline__ void mid_step(uint32_t row, uint32_t xs, uint32_t fs,
                 s[i] = pack2(f, f);
             }
             if constexpr (affine(MODE)) {
-                const float f = bf16_bits_to_f32(__shfl_sync(FULL, rawb[i], (lane & ~3u) | u));
+                const float f = __uint_as_float(i & 1u ? bv[i >> 1] & 0xFFFF0000u : bv[i >> 1] << 16);
                 b[i] = pack2(f, f);
             }
         }
@@ -259,7 +266,7 @@ __global__ void __launch_bounds__(MID_THREADS, 2) mid_product(const MidParams P)
         ptx::cp_async_commit();
     };
     // scales of unit q of a step, a step ahead, in registers
-    uint32_t raw[4], rawb[4] = {0u, 0u, 0u, 0u}, nraw[4], nrawb[4] = {0u, 0u, 0u, 0u};
+    uint32_t raw[2], rawb[2] = {0u, 0u}, nraw[4], nrawb[4] = {0u, 0u, 0u, 0u};
     auto fetch = [&](uint32_t j) {
         const uint32_t o = scale_entry<MODE>(tmin<uint32_t>(4u * j + q, nu - 1u), P.gshift);
 #pragma unroll
@@ -288,7 +295,10 @@ __global__ void __launch_bounds__(MID_THREADS, 2) mid_product(const MidParams P)
         __syncthreads();  // the step has landed, and the slot of the step before is free
         issue(j + RINGS - 1u, slot == 0u ? RINGS - 1u : slot - 1u);
 #pragma unroll
-        for (uint32_t i = 0; i < 4; i++) raw[i] = nraw[i], rawb[i] = nrawb[i];
+        for (uint32_t t = 0; t < 2; t++) {
+            raw[t] = nraw[2 * t] | nraw[2 * t + 1] << 16;
+            if constexpr (affine(MODE)) rawb[t] = nrawb[2 * t] | nrawb[2 * t + 1] << 16;
+        }
         if (j + 1u < steps) fetch(j + 1u);
         if (active) {
             const uint32_t on = slot * STAGE;
