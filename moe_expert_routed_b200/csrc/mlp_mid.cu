@@ -24,7 +24,8 @@
 namespace moe {
 namespace {
 
-constexpr uint32_t MID_THREADS = 256, MID_WARPS = 8, MID_ROWS = 256, MID_BLOCKS = 4;
+constexpr uint32_t MID_WARPS = 4, MID_CTAS = 4;  // of a CTA, and CTAs an SM
+constexpr uint32_t MID_THREADS = 32 * MID_WARPS, MID_ROWS = 32 * MID_WARPS, MID_BLOCKS = 4;
 constexpr uint32_t MID_PAIRS = 8 * MID_BLOCKS;  // of a tile
 
 // Bytes of a row's 128 codes in a stage: padded so that the lanes' quarters of eight rows
@@ -37,9 +38,9 @@ __host__ __device__ constexpr uint32_t x_line(int m) { return m == M_NV ? 288u :
 __host__ __device__ constexpr uint32_t stage_bytes(int m) {
     return MID_ROWS * line(m) + MID_PAIRS * (x_line(m) + 32u);
 }
-// Stages that leave room for two CTAs an SM.
-__host__ __device__ constexpr uint32_t ring(int m) { return 3u * stage_bytes(m) <= 112u * 1024u ? 3u : 2u; }
-constexpr uint32_t HB = 132;  // floats of a pair's 128 columns of h in the epilogue
+// Stages that leave room for the SM's CTAs.
+__host__ __device__ constexpr uint32_t ring(int m) { return 3u * stage_bytes(m) <= 224u * 1024u / MID_CTAS ? 3u : 2u; }
+constexpr uint32_t HC = 16 * MID_WARPS, HB = HC + 4;  // UP: columns of h, floats of a pair's in the epilogue
 
 struct MidParams {
     const uint8_t *w, *s, *a;    // packed codes, scales, affine biases or scale2 (or codebook)
@@ -191,7 +192,7 @@ __device__ __forceinline__ void mid_step(uint32_t row, uint32_t xs, uint32_t fs,
 
 // grid (blocks of 256 rows, tiles).
 template <int MODE, bool UP>
-__global__ void __launch_bounds__(MID_THREADS, 2) mid_product(const MidParams P) {
+__global__ void __launch_bounds__(MID_THREADS, MID_CTAS) mid_product(const MidParams P) {
     constexpr uint32_t LINE = line(MODE), XL = x_line(MODE), STAGE = stage_bytes(MODE), RINGS = ring(MODE);
     constexpr uint32_t X_AT = MID_ROWS * LINE, F_AT = X_AT + MID_PAIRS * XL;
     static_assert(MID_PAIRS * HB * 4u <= RINGS * STAGE, "the epilogue's h takes the ring's room");
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(MID_THREADS, 2) mid_product(const MidParams P)
     const uint32_t nu = P.k / 32u, steps = (nu + 3u) / 4u, srow = scale_bytes(MODE, P.groups);
 
     // the lane's rows r, r + 8 of two tiles; UP: gate and up of 8 columns are a tile
-    const uint32_t row0 = blockIdx.x * (UP ? 128u : 256u) + warp * (UP ? 16u : 32u);
+    const uint32_t row0 = blockIdx.x * (UP ? HC : MID_ROWS) + warp * (UP ? 16u : 32u);
     const bool active = row0 < P.n;
     const size_t first = (size_t)e * (UP ? 2u : 1u) * P.n + (active ? row0 : 0u) + r;
     const size_t dr = UP ? P.n : 8u, dt = UP ? 8u : 16u;  // rows on to the lane's second, and to the next tile
@@ -212,14 +213,17 @@ __global__ void __launch_bounds__(MID_THREADS, 2) mid_product(const MidParams P)
     const uint32_t sm0 = ptx::smem_u32(sm);
 
     // half a warp copies a pair's values, a quad the (factor, sum)s of a pair's four units
-    auto image = [&](uint32_t pr) {
+    constexpr uint32_t VI = MID_PAIRS / (2u * MID_WARPS), FI = (MID_PAIRS + 8u * MID_WARPS - 1u) / (8u * MID_WARPS);
+    auto image = [&](uint32_t pr) {  // in units of 16 bytes
         const uint32_t at = place + (pr < np ? pr : 0u);
-        const size_t img = UP ? __ldg(P.sorted_pairs + at) / P.S : at;
-        return P.x + img * steps * step_bytes(1);
+        return (UP ? __ldg(P.sorted_pairs + at) / P.S : at) * (steps * (step_bytes(1) / 16u));
     };
-    const uint32_t vp = 2u * warp + (lane >> 4), fp = 8u * warp + r;  // and vp + 16
-    const uint8_t *const v0 = image(vp) + (lane & 15u) * 16u, *const v1 = image(vp + 16u) + (lane & 15u) * 16u;
-    const uint8_t *const f0 = image(fp) + 256u + q * 8u;
+    const uint32_t vp = 2u * warp + (lane >> 4), fp = 8u * warp + r;
+    uint32_t vo[VI], fo[FI];
+#pragma unroll
+    for (uint32_t i = 0; i < VI; i++) vo[i] = image(vp + 2u * MID_WARPS * i) + (lane & 15u);
+#pragma unroll
+    for (uint32_t i = 0; i < FI; i++) fo[i] = image(fp + 8u * MID_WARPS * i) + 16u;
     const uint32_t vd = X_AT + vp * XL + (lane & 15u) * 16u, fd = F_AT + (q * MID_PAIRS + fp) * 8u;
     // 3-bit codes: the 16-byte blocks of memory that hold a step's 14 words
     const uint32_t rw = P.row_bytes / 4u, misplaced = MODE == M_CB3 ? r * rw : 0u;
@@ -258,10 +262,15 @@ __global__ void __launch_bounds__(MID_THREADS, 2) mid_product(const MidParams P)
                     }
                 }
             }
-            const uint32_t o = j * step_bytes(1);
-            ptx::cp_async_16_if(vp < np, st + vd, v0 + o, 16u);
-            ptx::cp_async_16_if(vp + 16u < np, st + vd + 16u * XL, v1 + o, 16u);
-            if (fp < np) ptx::cp_async_8(st + fd, f0 + o, 8u);
+            const uint8_t *const x = P.x + j * step_bytes(1);
+#pragma unroll
+            for (uint32_t i = 0; i < VI; i++)
+                ptx::cp_async_16_if(vp + 2u * MID_WARPS * i < np, st + vd + 2u * MID_WARPS * i * XL,
+                                    x + (size_t)vo[i] * 16u, 16u);
+#pragma unroll
+            for (uint32_t i = 0; i < FI; i++)
+                if (fp + 8u * MID_WARPS * i < np)
+                    ptx::cp_async_8(st + fd + 64u * MID_WARPS * i, x + (size_t)fo[i] * 16u + q * 8u, 8u);
         }
         ptx::cp_async_commit();
     };
@@ -355,28 +364,31 @@ __global__ void __launch_bounds__(MID_THREADS, 2) mid_product(const MidParams P)
             }
         }
         __syncthreads();
-        // a warp writes a unit of 32 columns of a pair: one step's images, 4 units, a CTA
-        const uint32_t units = tmin<uint32_t>((P.n - blockIdx.x * 128u) / 32u, 4u), hsteps = (P.n + 127u) / 128u;
-        for (uint32_t o = warp; o < 4u * np; o += MID_WARPS) {
-            const uint32_t pr = o >> 2, un = o & 3u;
-            float h = un < units ? hb[pr * HB + un * 32u + lane] : 0.f, sum = h;  // zeros past the last column
+        // a warp writes a unit of 32 columns of a pair; the row of CTAs all of the last step's
+        constexpr uint32_t HU = HC / 32u;
+        const uint32_t u0 = blockIdx.x * HU, units = P.n / 32u, hsteps = (units + 3u) / 4u;
+        const uint32_t end = blockIdx.x + 1u == gridDim.x ? 4u * hsteps : u0 + HU;
+        for (uint32_t o = warp; o < (end - u0) * np; o += MID_WARPS) {
+            const uint32_t pr = o / (end - u0), un = u0 + o % (end - u0);
+            float h = un < units ? hb[pr * HB + (un - u0) * 32u + lane] : 0.f, sum = h;  // zeros past the last column
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(FULL, sum, d);
             float scale, factor;
             unit_scale(__reduce_max_sync(FULL, __float_as_uint(h) & 0x7FFFFFFFu), scale, factor);
             h *= scale;
             if (P.order == 1 && (lane & 1u)) h *= 0.0625f;  // meets a 16-fold pair
-            uint8_t *img = (uint8_t *)P.out + ((size_t)(place + pr) * hsteps + blockIdx.x) * step_bytes(1);
-            ((uint16_t *)(img + un * 64u))[b_place(P.order, lane)] = __half_as_ushort(__float2half_rn(h));
-            if (lane == 0) ((float2 *)(img + 256u))[un] = make_float2(factor, sum);
+            uint8_t *img = (uint8_t *)P.out + ((size_t)(place + pr) * hsteps + (un >> 2)) * step_bytes(1);
+            ((uint16_t *)(img + (un & 3u) * 64u))[b_place(P.order, lane)] = __half_as_ushort(__float2half_rn(h));
+            if (lane == 0) ((float2 *)(img + 256u))[un & 3u] = make_float2(factor, sum);
         }
     }
 }
 
+constexpr uint32_t IMAGE_WARPS = 8;
 // The tokens' images, in the order of MODE's codes. grid (tokens, blocks of 8 steps).
 template <int MODE>
-__global__ void __launch_bounds__(MID_THREADS) mid_images(const void *x, int dt, uint32_t k, uint8_t *img) {
-    const uint32_t lane = threadIdx.x & 31u, j = blockIdx.y * MID_WARPS + (threadIdx.x >> 5), c = j * 128u + 4u * lane;
+__global__ void __launch_bounds__(32 * IMAGE_WARPS) mid_images(const void *x, int dt, uint32_t k, uint8_t *img) {
+    const uint32_t lane = threadIdx.x & 31u, j = blockIdx.y * IMAGE_WARPS + (threadIdx.x >> 5), c = j * 128u + 4u * lane;
     const uint32_t steps = (k + 127u) / 128u;
     if (j >= steps) return;
     const float4 v = c < k ? load_x4(x, dt, (size_t)blockIdx.x * k + c) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -426,7 +438,8 @@ uint64_t mlp_mid_workspace(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t
 
 bool mlp_mid_supported(const MlpArgs &a) {
     const uint64_t R = (uint64_t)a.m * a.S;
-    return R <= mid_limit(a.E) && a.E <= MOE_ROUTE_MAX_EXPERTS && a.x_dtype != DT_F32 && a.out_dtype != DT_F32 &&
+    // (images are addressed by 32 bits in steps of 16 bytes)
+    return R <= mid_limit(a.E) && R * ((tmax(a.hidden, a.inter) + 127ull) / 128u) * (step_bytes(1) / 16u) < 1ull << 32 && a.E <= MOE_ROUTE_MAX_EXPERTS && a.x_dtype != DT_F32 && a.out_dtype != DT_F32 &&
            mode_of(*a.gate_up, a.hidden) >= 0 && mode_of(*a.down, a.inter) >= 0 && ((uintptr_t)a.x & 7u) == 0;
 }
 
@@ -444,11 +457,11 @@ cudaError_t launch_mlp_mid(const MlpArgs &a, uint8_t *ws, uint8_t *own, cudaStre
                                  0, 0, st);
     if (e != cudaSuccess) return e;
     const int m1 = mode_of(*a.gate_up, a.hidden), m2 = mode_of(*a.down, a.inter);
-    const dim3 grid(a.m, ((a.hidden + 127u) / 128u + MID_WARPS - 1u) / MID_WARPS);
-    if (order_of(m1) == 1) mid_images<M_A4><<<grid, MID_THREADS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi);
-    else if (order_of(m1) == 2) mid_images<M_A8><<<grid, MID_THREADS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi);
-    else if (m1 == M_A6) mid_images<M_A6><<<grid, MID_THREADS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi);
-    else mid_images<M_NV><<<grid, MID_THREADS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi);
+    const dim3 grid(a.m, ((a.hidden + 127u) / 128u + IMAGE_WARPS - 1u) / IMAGE_WARPS);
+    if (order_of(m1) == 1) mid_images<M_A4><<<grid, 32 * IMAGE_WARPS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi);
+    else if (order_of(m1) == 2) mid_images<M_A8><<<grid, 32 * IMAGE_WARPS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi);
+    else if (m1 == M_A6) mid_images<M_A6><<<grid, 32 * IMAGE_WARPS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi);
+    else mid_images<M_NV><<<grid, 32 * IMAGE_WARPS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
     MidParams P{};
