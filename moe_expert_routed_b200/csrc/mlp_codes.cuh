@@ -296,6 +296,24 @@ __device__ __forceinline__ float4 load_x4(const void *x, int dt, size_t i) {
                        f16_bits_to_f32(v.y >> 16));
 }
 
+// Four values of lane l (4l .. 4l+3 of a step) times `scale`, in the order of MODE's codes.
+template <int MODE, int PLANES>
+__device__ __forceinline__ float4 in_order(float4 v, float scale, uint32_t lane) {
+    if constexpr (order_of(MODE) == 1) {
+        // a word's pairs are (0, 4), (1, 5) for the even lane and (2, 6), (3, 7) for the odd one
+        const bool odd = lane & 1u;
+        const float s0 = odd ? v.x : v.z, s1 = odd ? v.y : v.w;
+        const float r0 = __shfl_xor_sync(FULL, s0, 1), r1 = __shfl_xor_sync(FULL, s1, 1);
+        const float sixteenth = centred(MODE, PLANES) ? scale : scale * 0.0625f;
+        return odd ? make_float4(r0 * scale, v.z * scale, r1 * sixteenth, v.w * sixteenth)
+                   : make_float4(v.x * scale, r0 * scale, v.y * sixteenth, r1 * sixteenth);
+    } else if constexpr (order_of(MODE) == 2) {
+        return make_float4(v.x * scale, v.z * scale, v.y * scale, v.w * scale);
+    } else {
+        return make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
+    }
+}
+
 // A warp writes one step image: lane l holds values 4l .. 4l+3 (unit l / 8).
 template <int MODE, int PLANES>
 __device__ __forceinline__ void write_step(uint8_t *dst, float4 v, uint32_t lane) {
@@ -310,19 +328,7 @@ __device__ __forceinline__ void write_step(uint8_t *dst, float4 v, uint32_t lane
     }
     float scale, factor;
     unit_scale(mb, scale, factor);
-    if constexpr (order_of(MODE) == 1) {
-        // a word's pairs are (0, 4), (1, 5) for the even lane and (2, 6), (3, 7) for the odd one
-        const bool odd = lane & 1u;
-        const float s0 = odd ? v.x : v.z, s1 = odd ? v.y : v.w;
-        const float r0 = __shfl_xor_sync(FULL, s0, 1), r1 = __shfl_xor_sync(FULL, s1, 1);
-        const float sixteenth = centred(MODE, PLANES) ? scale : scale * 0.0625f;
-        v = odd ? make_float4(r0 * scale, v.z * scale, r1 * sixteenth, v.w * sixteenth)
-                : make_float4(v.x * scale, r0 * scale, v.y * sixteenth, r1 * sixteenth);
-    } else if constexpr (order_of(MODE) == 2) {
-        v = make_float4(v.x * scale, v.z * scale, v.y * scale, v.w * scale);
-    } else {
-        v = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
-    }
+    v = in_order<MODE, PLANES>(v, scale, lane);
     uint2 *p = (uint2 *)(dst + lane * 8u);
 #pragma unroll
     for (int k = 0; k < PLANES; k++, p += 32) {

@@ -27,6 +27,9 @@ namespace {
 constexpr uint32_t MID_WARPS = 4, MID_CTAS = 4;  // of a CTA, and CTAs an SM
 constexpr uint32_t MID_THREADS = 32 * MID_WARPS, MID_ROWS = 32 * MID_WARPS, MID_BLOCKS = 4;
 constexpr uint32_t MID_PAIRS = 8 * MID_BLOCKS;  // of a tile
+// Affine codes are f16 integers times 2^-24; the sums of x that meet the biases are scaled
+// alike, and the results back.
+constexpr float CODE_UNIT = 16777216.f;
 
 // Bytes of a row's 128 codes in a stage: padded so that the lanes' quarters of eight rows
 // lie in different banks (3 bits: the 16-byte blocks that hold 14 words of 10 codes; 6 bits: two lanes can meet).
@@ -46,6 +49,7 @@ struct MidParams {
     const uint8_t *w, *s, *a;    // packed codes, scales, affine biases or scale2 (or codebook)
     const void *bias;            // expert biases, or null
     const uint8_t *x;            // images: [token] (UP), [place among the sorted pairs] (DOWN)
+    const float *factor;         // UP: of the tokens' values
     const uint32_t *offsets, *sorted_pairs, *tiles, *tile_count;
     void *out;                   // UP: images of h by sorted place; DOWN: z [pair][n] f32
     uint32_t k, n, S;            // n: rows of out (UP: of gate, the up rows follow)
@@ -75,6 +79,12 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return d;
 }
 
+__device__ __forceinline__ uint64_t lds64x(uint32_t a) {
+    uint64_t v;
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(a));
+    return v;
+}
+
 // This lane's 8 codes of a unit from its row's line: quarter q, or (NVFP4) four of each
 // scale's 16; `code`: 3-bit codes before the quarter in the line.
 template <int MODE>
@@ -99,8 +109,7 @@ __device__ __forceinline__ void quarter(uint32_t at, uint32_t u, uint32_t q, uin
     }
 }
 
-// A unit's scale as it is stored (NVFP4: two), and as f32; affine codes are f16 integers
-// times 2^-24.
+// A unit's scale as it is stored (NVFP4: two), and as f32.
 template <int MODE>
 __device__ __forceinline__ uint32_t raw_scale(const uint8_t *p) {
     // volatile: requested where it stands, a step ahead of its use
@@ -111,16 +120,16 @@ __device__ __forceinline__ uint32_t raw_scale(const uint8_t *p) {
 }
 template <int MODE>
 __device__ __forceinline__ float scale_f32(uint32_t v) {
-    if constexpr (affine(MODE)) return bf16_bits_to_f32(v) * 16777216.f;
+    if constexpr (affine(MODE)) return bf16_bits_to_f32(v);
     else if constexpr (codebook(MODE)) return f16_bits_to_f32(v);
     else return e8m0_to_f32(v);
 }
 
 // The warp's 32 rows x a step x 8 NT pairs; past the last column codes and x are zero. row: shared address of the
-// lane's first row, xs, fs: of its part of the pairs' values and (factor, sum)s; c0: 3-bit codes
+// lane's first row, xs, fs: of its part of the pairs' values, and of their factors and sums; c0: 3-bit codes
 // before the step in the line; raw, rawb: unit q's scales of the lane's four
 // rows, two in a register.
-template <int MODE, int NT>
+template <int MODE, bool UP, int NT>
 __device__ __forceinline__ void mid_step(uint32_t row, uint32_t xs, uint32_t fs, uint32_t c0,
                                          const uint32_t (&raw)[2], const uint32_t (&rawb)[2], const Table<MODE> &tab,
                                          uint32_t lane, uint64_t (&acc)[2][2][MID_BLOCKS]) {
@@ -165,9 +174,9 @@ __device__ __forceinline__ void mid_step(uint32_t row, uint32_t xs, uint32_t fs,
             } else {
                 B = lds128(xs + n * 8u * x_line(MODE) + u * 64u);
             }
-            const uint4 F = lds128(fs + (u * MID_PAIRS + n * 8u) * 8u);
-            const uint64_t f = pack2(__uint_as_float(F.x), __uint_as_float(F.z));
-            const uint64_t sum = pack2(__uint_as_float(F.y), __uint_as_float(F.w));
+            uint64_t f = 0ull, sum = 0ull;
+            if constexpr (!UP) f = lds64x(fs + (u * MID_PAIRS + n * 8u) * 4u);
+            if constexpr (affine(MODE)) sum = lds64x(fs + ((4u + u) * MID_PAIRS + n * 8u) * 4u);
 #pragma unroll
             for (uint32_t t = 0; t < 2; t++) {
                 const uint32_t i = 2u * t;
@@ -179,10 +188,13 @@ __device__ __forceinline__ void mid_step(uint32_t row, uint32_t xs, uint32_t fs,
                 for (uint32_t h = 0; h < 2; h++) {
                     uint64_t &to = acc[t][h][n];
                     const uint64_t c2 = pack2(c[2 * h], c[2 * h + 1]);
-                    if constexpr (MODE == M_NV)
-                        to = fma2(f, fma2(s1[i + h], pack2(d[2 * h], d[2 * h + 1]), mul2(s[i + h], c2)), to);
-                    else
-                        to = fma2(s[i + h], mul2(f, c2), to);
+                    if constexpr (MODE == M_NV) {
+                        const uint64_t d2 = pack2(d[2 * h], d[2 * h + 1]);
+                        if constexpr (UP) to = fma2(s1[i + h], d2, fma2(s[i + h], c2, to));
+                        else to = fma2(f, fma2(s1[i + h], d2, mul2(s[i + h], c2)), to);
+                    } else {
+                        to = fma2(s[i + h], UP ? c2 : mul2(f, c2), to);
+                    }
                     if constexpr (affine(MODE)) to = fma2(b[i + h], sum, to);
                 }
             }
@@ -212,7 +224,7 @@ __global__ void __launch_bounds__(MID_THREADS, MID_CTAS) mid_product(const MidPa
     const uint8_t *const w0 = P.w + first * P.row_bytes, *const s0 = P.s + first * srow, *const b0 = P.a + first * srow;
     const uint32_t sm0 = ptx::smem_u32(sm);
 
-    // half a warp copies a pair's values, a quad the (factor, sum)s of a pair's four units
+    // half a warp copies a pair's values, a quad the factors and sums of a pair's four units
     constexpr uint32_t VI = MID_PAIRS / (2u * MID_WARPS), FI = (MID_PAIRS + 8u * MID_WARPS - 1u) / (8u * MID_WARPS);
     auto image = [&](uint32_t pr) {  // in units of 16 bytes
         const uint32_t at = place + (pr < np ? pr : 0u);
@@ -224,7 +236,7 @@ __global__ void __launch_bounds__(MID_THREADS, MID_CTAS) mid_product(const MidPa
     for (uint32_t i = 0; i < VI; i++) vo[i] = image(vp + 2u * MID_WARPS * i) + (lane & 15u);
 #pragma unroll
     for (uint32_t i = 0; i < FI; i++) fo[i] = image(fp + 8u * MID_WARPS * i) + 16u;
-    const uint32_t vd = X_AT + vp * XL + (lane & 15u) * 16u, fd = F_AT + (q * MID_PAIRS + fp) * 8u;
+    const uint32_t vd = X_AT + vp * XL + (lane & 15u) * 16u, fd = F_AT + (q * MID_PAIRS + fp) * 4u;
     // 3-bit codes: the 16-byte blocks of memory that hold a step's 14 words
     const uint32_t rw = P.row_bytes / 4u, misplaced = MODE == M_CB3 ? r * rw : 0u;
     auto issue = [&](uint32_t j, uint32_t slot) {
@@ -269,8 +281,12 @@ __global__ void __launch_bounds__(MID_THREADS, MID_CTAS) mid_product(const MidPa
                                     x + (size_t)vo[i] * 16u, 16u);
 #pragma unroll
             for (uint32_t i = 0; i < FI; i++)
-                if (fp + 8u * MID_WARPS * i < np)
-                    ptx::cp_async_8(st + fd + 64u * MID_WARPS * i, x + (size_t)fo[i] * 16u + q * 8u, 8u);
+                if ((!UP || affine(MODE)) && fp + 8u * MID_WARPS * i < np) {
+                    const uint8_t *const g = x + (size_t)fo[i] * 16u + q * 4u;
+                    const uint32_t d = st + fd + 32u * MID_WARPS * i;
+                    if constexpr (!UP) ptx::cp_async_4(d, g, 4u);
+                    if constexpr (affine(MODE)) ptx::cp_async_4(d + 16u * MID_PAIRS, g + 16u, 4u);
+                }
         }
         ptx::cp_async_commit();
     };
@@ -297,7 +313,7 @@ __global__ void __launch_bounds__(MID_THREADS, MID_CTAS) mid_product(const MidPa
         for (uint32_t n = 0; n < MID_BLOCKS; n++) acc[t >> 1][t & 1][n] = 0ull;
 
     const uint32_t row = sm0 + (warp * 32u + r) * LINE, xs = sm0 + X_AT + r * XL + q * (MODE == M_NV ? 8u : 16u),
-                   fs = sm0 + F_AT + q * 16u;
+                   fs = sm0 + F_AT + q * 8u;
     uint32_t slot = 0;
     for (uint32_t j = 0; j < steps; j++) {
         wait_groups<(int)RINGS - 2>();
@@ -313,17 +329,17 @@ __global__ void __launch_bounds__(MID_THREADS, MID_CTAS) mid_product(const MidPa
             const uint32_t on = slot * STAGE;
             const uint32_t c0 = MODE == M_CB3 ? 128u * j % 10u : 0u, o = MODE == M_CB3 ? (misplaced + 128u * j / 10u) % 4u * 4u : 0u;
             switch (nt) {
-                case 1: mid_step<MODE, 1>(row + on + o, xs + on, fs + on, c0, raw, rawb, tab, lane, acc); break;
-                case 2: mid_step<MODE, 2>(row + on + o, xs + on, fs + on, c0, raw, rawb, tab, lane, acc); break;
-                case 3: mid_step<MODE, 3>(row + on + o, xs + on, fs + on, c0, raw, rawb, tab, lane, acc); break;
-                default: mid_step<MODE, 4>(row + on + o, xs + on, fs + on, c0, raw, rawb, tab, lane, acc);
+                case 1: mid_step<MODE, UP, 1>(row + on + o, xs + on, fs + on, c0, raw, rawb, tab, lane, acc); break;
+                case 2: mid_step<MODE, UP, 2>(row + on + o, xs + on, fs + on, c0, raw, rawb, tab, lane, acc); break;
+                case 3: mid_step<MODE, UP, 3>(row + on + o, xs + on, fs + on, c0, raw, rawb, tab, lane, acc); break;
+                default: mid_step<MODE, UP, 4>(row + on + o, xs + on, fs + on, c0, raw, rawb, tab, lane, acc);
             }
         }
         slot = slot + 1u == RINGS ? 0u : slot + 1u;
     }
     wait_groups<0>();
 
-    const float s2 = MODE == M_NV ? __ldg((const float *)P.a + e) : 1.f;
+    const float s2 = MODE == M_NV ? __ldg((const float *)P.a + e) : affine(MODE) ? CODE_UNIT : 1.f;
     if constexpr (!UP) {
         if (!active) return;
         float *const z = (float *)P.out;
@@ -349,6 +365,12 @@ __global__ void __launch_bounds__(MID_THREADS, MID_CTAS) mid_product(const MidPa
         __syncthreads();  // every warp has left the ring
         float *const hb = (float *)sm;
         if (active) {
+            float tf[MID_BLOCKS][2];
+#pragma unroll
+            for (uint32_t n = 0; n < 2 * MID_BLOCKS; n++) {
+                const uint32_t pr = 4u * (n & ~1u) + 2u * q + (n & 1u);
+                tf[n >> 1][n & 1] = pr < np ? __ldg(P.factor + __ldg(P.sorted_pairs + place + pr) / P.S) : 0.f;
+            }
 #pragma unroll
             for (uint32_t t = 0; t < 2; t++) {
                 const uint32_t c = warp * 16u + 8u * t + r;
@@ -358,8 +380,9 @@ __global__ void __launch_bounds__(MID_THREADS, MID_CTAS) mid_product(const MidPa
                 for (uint32_t n = 0; n < MID_BLOCKS; n++) {
                     const float2 g = unpack2(acc[t][0][n]), u = unpack2(acc[t][1][n]);
                     const uint32_t pr = 8u * n + 2u * q;
-                    if (pr < np) hb[pr * HB + c] = glu_act(P.act, fmaf(g.x, s2, bg)) * fmaf(u.x, s2, bu);
-                    if (pr + 1u < np) hb[(pr + 1u) * HB + c] = glu_act(P.act, fmaf(g.y, s2, bg)) * fmaf(u.y, s2, bu);
+                    if (pr < np) hb[pr * HB + c] = glu_act(P.act, fmaf(g.x * s2, tf[n][0], bg)) * fmaf(u.x * s2, tf[n][0], bu);
+                    if (pr + 1u < np)
+                        hb[(pr + 1u) * HB + c] = glu_act(P.act, fmaf(g.y * s2, tf[n][1], bg)) * fmaf(u.y * s2, tf[n][1], bu);
                 }
             }
         }
@@ -379,20 +402,49 @@ __global__ void __launch_bounds__(MID_THREADS, MID_CTAS) mid_product(const MidPa
             if (P.order == 1 && (lane & 1u)) h *= 0.0625f;  // meets a 16-fold pair
             uint8_t *img = (uint8_t *)P.out + ((size_t)(place + pr) * hsteps + (un >> 2)) * step_bytes(1);
             ((uint16_t *)(img + (un & 3u) * 64u))[b_place(P.order, lane)] = __half_as_ushort(__float2half_rn(h));
-            if (lane == 0) ((float2 *)(img + 256u))[un & 3u] = make_float2(factor, sum);
+            if (lane == 0) {
+                ((float *)(img + 256u))[un & 3u] = factor;
+                ((float *)(img + 272u))[un & 3u] = sum * (1.f / CODE_UNIT);
+            }
         }
     }
 }
 
 constexpr uint32_t IMAGE_WARPS = 8;
-// The tokens' images, in the order of MODE's codes. grid (tokens, blocks of 8 steps).
+// The tokens' images, in the order of MODE's codes, and the power of two of each. A CTA a
+// token: the largest |value| first, so that the products need no factor for each unit.
 template <int MODE>
-__global__ void __launch_bounds__(32 * IMAGE_WARPS) mid_images(const void *x, int dt, uint32_t k, uint8_t *img) {
-    const uint32_t lane = threadIdx.x & 31u, j = blockIdx.y * IMAGE_WARPS + (threadIdx.x >> 5), c = j * 128u + 4u * lane;
-    const uint32_t steps = (k + 127u) / 128u;
-    if (j >= steps) return;
-    const float4 v = c < k ? load_x4(x, dt, (size_t)blockIdx.x * k + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-    write_step<MODE, 1>(img + ((size_t)blockIdx.x * steps + j) * step_bytes(1), v, lane);
+__global__ void __launch_bounds__(32 * IMAGE_WARPS) mid_images(const void *x, int dt, uint32_t k, uint8_t *img, float *tf) {
+    __shared__ uint32_t most[IMAGE_WARPS];
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, steps = (k + 127u) / 128u;
+    const size_t row = (size_t)blockIdx.x * k;
+    uint32_t mb = 0u;
+    for (uint32_t c = 4u * threadIdx.x; c < k; c += 128u * IMAGE_WARPS) {
+        const uint32_t M = 0x7FFFFFFFu;
+        const float4 v = load_x4(x, dt, row + c);
+        mb = max(mb, max(max(__float_as_uint(v.x) & M, __float_as_uint(v.y) & M),
+                         max(__float_as_uint(v.z) & M, __float_as_uint(v.w) & M)));
+    }
+    mb = __reduce_max_sync(FULL, mb);
+    if (lane == 0) most[warp] = mb;
+    __syncthreads();
+    mb = __reduce_max_sync(FULL, most[lane % IMAGE_WARPS]);
+    float scale, factor;
+    unit_scale(mb, scale, factor);
+    if (threadIdx.x == 0) tf[blockIdx.x] = factor;
+    for (uint32_t j = warp; j < steps; j += IMAGE_WARPS) {
+        const uint32_t c = j * 128u + 4u * lane;
+        float4 v = c < k ? load_x4(x, dt, row + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        uint8_t *const to = img + ((size_t)blockIdx.x * steps + j) * step_bytes(1);
+        if constexpr (affine(MODE)) {
+            float sum = (v.x * scale + v.y * scale) + (v.z * scale + v.w * scale);
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(FULL, sum, d);
+            if ((lane & 7u) == 0u) ((float *)(to + 272u))[lane >> 3] = sum * (1.f / CODE_UNIT);
+        }
+        v = in_order<MODE, 1>(v, scale, lane);
+        ((uint2 *)to)[lane] = make_uint2(to_f16x2(v.x, v.y), to_f16x2(v.z, v.w));
+    }
 }
 
 template <int MODE, bool UP>
@@ -433,7 +485,7 @@ static uint64_t mid_limit(uint32_t E) { return tmin<uint64_t>((uint64_t)MOE_MLP_
 uint64_t mlp_mid_workspace(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t S, uint32_t E) {
     // with more pairs than it takes, what fewer pairs in the same workspace need
     const uint64_t R = tmin<uint64_t>((uint64_t)m * S, mid_limit(E)), tokens = tmin<uint64_t>(m, R);
-    return al256(8ull * tiles_of(R, E)) + images(tokens, hidden) + images(R, inter) + R * hidden * 4ull;
+    return al256(8ull * tiles_of(R, E)) + images(tokens, hidden) + images(R, inter) + al256(4ull * tokens) + R * hidden * 4ull;
 }
 
 bool mlp_mid_supported(const MlpArgs &a) {
@@ -451,23 +503,22 @@ cudaError_t launch_mlp_mid(const MlpArgs &a, uint8_t *ws, uint8_t *own, cudaStre
     uint32_t *const counts = (uint32_t *)(ws + L.counts), *const offsets = (uint32_t *)(ws + L.offsets);
     uint32_t *const sp = (uint32_t *)(ws + L.sorted_pairs), *const tiles = (uint32_t *)own;
     uint8_t *const xi = own + al256(8ull * max_tiles), *const hi = xi + images(a.m, a.hidden);
-    float *const z = (float *)(hi + images(R, a.inter));
+    float *const tf = (float *)(hi + images(R, a.inter)), *const z = tf + al256(4ull * a.m) / 4u;
     cudaError_t e = launch_route(a.ids, R, a.E, MID_PAIRS, counts, offsets, sp, tiles, tc, max_tiles,
                                  (uint32_t *)(ws + L.chunk_hist), (uint32_t *)(ws + L.chunk_base), L.chunks, err, nullptr,
                                  0, 0, st);
     if (e != cudaSuccess) return e;
     const int m1 = mode_of(*a.gate_up, a.hidden), m2 = mode_of(*a.down, a.inter);
-    const dim3 grid(a.m, ((a.hidden + 127u) / 128u + IMAGE_WARPS - 1u) / IMAGE_WARPS);
-    if (order_of(m1) == 1) mid_images<M_A4><<<grid, 32 * IMAGE_WARPS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi);
-    else if (order_of(m1) == 2) mid_images<M_A8><<<grid, 32 * IMAGE_WARPS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi);
-    else if (m1 == M_A6) mid_images<M_A6><<<grid, 32 * IMAGE_WARPS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi);
-    else mid_images<M_NV><<<grid, 32 * IMAGE_WARPS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi);
+    if (order_of(m1) == 1) mid_images<M_A4><<<a.m, 32 * IMAGE_WARPS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi, tf);
+    else if (order_of(m1) == 2) mid_images<M_A8><<<a.m, 32 * IMAGE_WARPS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi, tf);
+    else if (m1 == M_A6) mid_images<M_A6><<<a.m, 32 * IMAGE_WARPS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi, tf);
+    else mid_images<M_NV><<<a.m, 32 * IMAGE_WARPS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi, tf);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
     MidParams P{};
     P.w = (const uint8_t *)a.gate_up->packed; P.s = (const uint8_t *)a.gate_up->scales;
     P.a = (const uint8_t *)a.gate_up->aux; P.bias = a.gate_up->bias; P.bias_dtype = (int)a.gate_up->bias_dtype;
-    P.x = xi; P.out = hi;
+    P.x = xi; P.factor = tf; P.out = hi;
     P.offsets = offsets; P.sorted_pairs = sp; P.tiles = tiles; P.tile_count = tc;
     P.k = a.hidden; P.n = a.inter; P.S = a.S;
     P.row_bytes = (uint32_t)moe_packed_row_bytes(a.gate_up->fmt, a.gate_up->bits, a.hidden);

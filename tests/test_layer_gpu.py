@@ -254,6 +254,33 @@ def test_mlp_wide_range_of_x(x_dtype, m):
     check(L, layer(*inputs(L)), DT_F32)
 
 
+@pytest.mark.parametrize("x_dtype", [DT_BF16, DT_F16])
+@pytest.mark.parametrize("fmt", sorted(FORMATS))
+def test_mlp_tens_of_pairs_an_expert(fmt, x_dtype):
+    """Sizes between the few-token kernels and the grouped products: tiles of every number
+    of blocks of 8 pairs, more than one tile an expert, an expert without pairs, rows of
+    weights and of values that end inside a step; values of very different sizes."""
+    f, bits, gs = FORMATS[fmt]
+    hidden, inter = (320, 224) if gs < 64 else (320, 192) if gs == 64 else (384, 128)
+    L = LR.Layer(m=60, hidden=hidden, inter=inter, top_k=3, E=6, fmt=f, bits=bits, gs=gs, x_dtype=x_dtype, seed=5,
+                 bias=True)
+    ids = np.tile(np.arange(3), (60, 1))
+    ids[:50, 2] = 3 + (np.arange(50) >= 11)  # 60, 60, 10, 11 and 39 pairs, none
+    L.gu = L.gu.with_ids(ids.astype(np.uint32))
+    x = torch.randn(60, hidden, generator=torch.Generator().manual_seed(3), dtype=torch.float64)
+    x[7] *= torch.exp2(torch.linspace(-12, 6, hidden // 32)).repeat_interleave(32)
+    x[9] = 0
+    t = x.to(LR.TORCH_DT[x_dtype])
+    L.gu = L.gu.with_x(t.view(torch.int16).numpy().view(np.uint16))
+    L.bias = (L.bias[0], torch.from_numpy(L.bias[1]).to(torch.bfloat16).float().numpy())
+    res = torch.from_numpy(L.res).to(t.dtype).cuda()
+    layer = build(L, out_dtype=x_dtype, max_tokens=61)
+    out = layer(*inputs(L), residual=res)
+    check(L, out, x_dtype, res.double().cpu().numpy())
+    assert torch.equal(out, layer(*inputs(L), residual=res))
+    assert M.poll_error(layer.workspace) == 0
+
+
 @pytest.mark.parametrize("fmt", sorted(FORMATS))
 @pytest.mark.parametrize("m", [1, 7])
 def test_mlp_few_tokens_keep_32_bits(fmt, m):
