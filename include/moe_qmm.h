@@ -408,7 +408,7 @@ typedef struct {
  */
 #define MOE_MLP_FEW_TOKENS 64u
 #define MOE_MLP_FEW_PAIRS 512u
-#define MOE_MLP_MID_PAIRS 64u
+#define MOE_MLP_MID_PAIRS 32u
 size_t moe_mlp_workspace_bytes(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t n_expert_used,
                                uint32_t num_experts, moe_dtype x_dtype);
 moe_status moe_mlp(const void *x, const uint32_t *ids, const float *weights, const moe_expert_weights *gate_up,

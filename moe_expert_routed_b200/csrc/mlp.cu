@@ -92,18 +92,22 @@ moe_status moe_mlp(const void *x, const uint32_t *ids, const float *weights, con
     void *h = ws + L.h, *z = ws + L.z;
     const MlpArgs a{x,      ids,   weights, gate_up,       down,        residual,     out,           m,
                     hidden, inter, n_expert_used, num_experts, (int)x_dtype, (int)out_dtype, (int)act};
-    // The few-token kernels multiply every pair with its expert's rows on mma.sync, four
-    // pairs' worth of tensor work for one, so their time grows with the pairs an expert
-    // has; the grouped GEMM's hardly does. Measured with 2,816 x 704 experts, few against
-    // grouped: at 4 pairs an expert 110 / 177 us (32 experts, affine 4 bits), 116 / 128
-    // (NVFP4), 147 / 180 (affine 8 bits); at 8 171 / 179, 179 / 131, 268 / 183. With up to 64
-    // pairs the routing and the launches of the grouped path cost more: 8 experts, 64
-    // pairs 49 / 79, 52 / 63, 66 / 83.
-    const bool few = path == MOE_PATH_DECODE || R <= 64u || R <= 4ull * num_experts;
-    if (few && path != MOE_PATH_GROUPED && mlp_few_supported(a))
+    // The few-token kernels have four pairs' worth of tensor work for one and no routing;
+    // mlp_mid.cu's products read and expand an expert's weights once for 24 pairs after it.
+    // Measured with 2,816 x 704 experts, few against mid, us: 256 experts, half a pair an
+    // expert 101 / 151 (affine 4 bits), 103 / 131 (NVFP4), 204 / 207 (3-bit codebook), 222 / 170
+    // (affine 8 bits); 1 pair 184 / 218, 193 / 191, 379 / 312, 392 / 248; 2 pairs 289 / 286, 311 /
+    // 250, 534 / 415, 604 / 324. 8 experts: 16 pairs in all 23 / 40, 38 / 50 (codebook), 32 pairs
+    // 42 / 43, 48 / 51, 64 pairs 61 / 46, 70 / 56. Where mlp_mid.cu does not apply (32-bit types),
+    // few against grouped: 4 pairs an expert 110 / 177, 116 / 128, 147 / 180 (affine 8 bits),
+    // 8 171 / 179, 179 / 131, 268 / 183; 64 pairs of 8 experts 49 / 79, 52 / 63, 66 / 83.
+    const bool mid = path == MOE_PATH_AUTO && mlp_mid_supported(a);
+    auto narrow = [](const moe_expert_weights *w) { return w->bits == 4 && w->fmt != MOE_FMT_CODEBOOK; };
+    const uint64_t few_to = !mid ? tmax<uint64_t>(64u, 4ull * num_experts)
+                                   : tmax<uint64_t>(32u, narrow(gate_up) && narrow(down) ? num_experts : num_experts / 2u);
+    if (path != MOE_PATH_GROUPED && (path == MOE_PATH_DECODE || R <= few_to) && mlp_few_supported(a))
         return launch_mlp_few(a, (uint32_t *)ws, h, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
-    if (path == MOE_PATH_AUTO && mlp_mid_supported(a))
-        return launch_mlp_mid(a, ws, ws + L.h, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    if (mid) return launch_mlp_mid(a, ws, ws + L.h, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     const moe_dtype hd = h_dtype((int)x_dtype);
     LayerProduct layer{0u};
     v = run_product(x, ids, *gate_up, h, m, hidden, 2u * inter, n_expert_used, num_experts, x_dtype, hd, (int)act,

@@ -1,6 +1,6 @@
 // mlp_mid.cu -- the gated expert MLP for some tens of pairs an expert: a block of
 // tokens, a batch of sequences. Two grouped products on mma.sync over the routing's tiles
-// of up to 32 pairs,
+// of up to 24 pairs,
 //   mid_product<UP>    h[p] = act(G_e x_t) * (U_e x_t)
 //   mid_product<DOWN>  z[p] = D_e h[p]
 // and the weighted sum of z.
@@ -24,8 +24,8 @@
 namespace moe {
 namespace {
 
-constexpr uint32_t MID_WARPS = 4, MID_CTAS = 4;  // of a CTA, and CTAs an SM
-constexpr uint32_t MID_THREADS = 32 * MID_WARPS, MID_ROWS = 32 * MID_WARPS, MID_BLOCKS = 4;
+constexpr uint32_t MID_WARPS = 4;
+constexpr uint32_t MID_THREADS = 32 * MID_WARPS, MID_ROWS = 32 * MID_WARPS, MID_BLOCKS = 3;
 constexpr uint32_t MID_PAIRS = 8 * MID_BLOCKS;  // of a tile
 // Affine codes are f16 integers times 2^-24; the sums of x that meet the biases are scaled
 // alike, and the results back.
@@ -41,8 +41,12 @@ __host__ __device__ constexpr uint32_t x_line(int m) { return m == M_NV ? 288u :
 __host__ __device__ constexpr uint32_t stage_bytes(int m) {
     return MID_ROWS * line(m) + MID_PAIRS * (x_line(m) + 32u);
 }
-// Stages that leave room for the SM's CTAs.
-__host__ __device__ constexpr uint32_t ring(int m) { return 3u * stage_bytes(m) <= 224u * 1024u / MID_CTAS ? 3u : 2u; }
+// CTAs an SM: five where their registers hold the expansion (tables of a codebook spill:
+// 326 us against 304 with four), as many as the stages leave room for.
+__host__ __device__ constexpr uint32_t ctas(int m) { return m == M_A8 ? 3u : m == M_A6 || codebook(m) ? 4u : 5u; }
+__host__ __device__ constexpr uint32_t ring(int m) {
+    return 3u * stage_bytes(m) <= 228u * 1024u / ctas(m) - 1024u ? 3u : 2u;
+}
 constexpr uint32_t HC = 16 * MID_WARPS, HB = HC + 4;  // UP: columns of h, floats of a pair's in the epilogue
 
 struct MidParams {
@@ -204,16 +208,19 @@ __device__ __forceinline__ void mid_step(uint32_t row, uint32_t xs, uint32_t fs,
 
 // grid (blocks of 256 rows, tiles).
 template <int MODE, bool UP>
-__global__ void __launch_bounds__(MID_THREADS, MID_CTAS) mid_product(const MidParams P) {
+__global__ void __launch_bounds__(MID_THREADS, ctas(MODE)) mid_product(const MidParams P) {
     constexpr uint32_t LINE = line(MODE), XL = x_line(MODE), STAGE = stage_bytes(MODE), RINGS = ring(MODE);
     constexpr uint32_t X_AT = MID_ROWS * LINE, F_AT = X_AT + MID_PAIRS * XL;
     static_assert(MID_PAIRS * HB * 4u <= RINGS * STAGE, "the epilogue's h takes the ring's room");
     extern __shared__ __align__(16) uint8_t sm[];
-    if (blockIdx.y >= __ldg(P.tile_count)) return;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    if (blockIdx.y >= *P.tile_count) return;
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u, r = lane >> 2, q = lane & 3u;
-    const uint32_t e = __ldg(P.tiles + 2u * blockIdx.y), r0 = __ldg(P.tiles + 2u * blockIdx.y + 1u);
-    const uint32_t place = __ldg(P.offsets + e) + r0;
-    const uint32_t np = tmin<uint32_t>(__ldg(P.offsets + e + 1u) - place, MID_PAIRS), nt = (np + 7u) / 8u;
+    // (plain loads: what the kernels before wrote, this one may have started beside them)
+    const uint32_t e = P.tiles[2u * blockIdx.y], r0 = P.tiles[2u * blockIdx.y + 1u];
+    const uint32_t place = P.offsets[e] + r0;
+    const uint32_t np = tmin<uint32_t>(P.offsets[e + 1u] - place, MID_PAIRS), nt = (np + 7u) / 8u;
     const uint32_t nu = P.k / 32u, steps = (nu + 3u) / 4u, srow = scale_bytes(MODE, P.groups);
 
     // the lane's rows r, r + 8 of two tiles; UP: gate and up of 8 columns are a tile
@@ -228,7 +235,7 @@ __global__ void __launch_bounds__(MID_THREADS, MID_CTAS) mid_product(const MidPa
     constexpr uint32_t VI = MID_PAIRS / (2u * MID_WARPS), FI = (MID_PAIRS + 8u * MID_WARPS - 1u) / (8u * MID_WARPS);
     auto image = [&](uint32_t pr) {  // in units of 16 bytes
         const uint32_t at = place + (pr < np ? pr : 0u);
-        return (UP ? __ldg(P.sorted_pairs + at) / P.S : at) * (steps * (step_bytes(1) / 16u));
+        return (UP ? P.sorted_pairs[at] / P.S : at) * (steps * (step_bytes(1) / 16u));
     };
     const uint32_t vp = 2u * warp + (lane >> 4), fp = 8u * warp + r;
     uint32_t vo[VI], fo[FI];
@@ -331,8 +338,7 @@ __global__ void __launch_bounds__(MID_THREADS, MID_CTAS) mid_product(const MidPa
             switch (nt) {
                 case 1: mid_step<MODE, UP, 1>(row + on + o, xs + on, fs + on, c0, raw, rawb, tab, lane, acc); break;
                 case 2: mid_step<MODE, UP, 2>(row + on + o, xs + on, fs + on, c0, raw, rawb, tab, lane, acc); break;
-                case 3: mid_step<MODE, UP, 3>(row + on + o, xs + on, fs + on, c0, raw, rawb, tab, lane, acc); break;
-                default: mid_step<MODE, UP, 4>(row + on + o, xs + on, fs + on, c0, raw, rawb, tab, lane, acc);
+                default: mid_step<MODE, UP, 3>(row + on + o, xs + on, fs + on, c0, raw, rawb, tab, lane, acc);
             }
         }
         slot = slot + 1u == RINGS ? 0u : slot + 1u;
@@ -353,7 +359,7 @@ __global__ void __launch_bounds__(MID_THREADS, MID_CTAS) mid_product(const MidPa
             for (uint32_t k = 0; k < 2; k++) {
                 const uint32_t pr = 8u * n + 2u * q + k;
                 if (pr < np) {
-                    float *const to = z + (size_t)__ldg(P.sorted_pairs + place + pr) * P.n + row0 + r;
+                    float *const to = z + (size_t)P.sorted_pairs[place + pr] * P.n + row0 + r;
 #pragma unroll
                     for (uint32_t i = 0; i < 4; i++) {
                         const float2 v = unpack2(acc[i >> 1][i & 1][n]);
@@ -369,7 +375,7 @@ __global__ void __launch_bounds__(MID_THREADS, MID_CTAS) mid_product(const MidPa
 #pragma unroll
             for (uint32_t n = 0; n < 2 * MID_BLOCKS; n++) {
                 const uint32_t pr = 4u * (n & ~1u) + 2u * q + (n & 1u);
-                tf[n >> 1][n & 1] = pr < np ? __ldg(P.factor + __ldg(P.sorted_pairs + place + pr) / P.S) : 0.f;
+                tf[n >> 1][n & 1] = pr < np ? P.factor[P.sorted_pairs[place + pr] / P.S] : 0.f;
             }
 #pragma unroll
             for (uint32_t t = 0; t < 2; t++) {
@@ -411,10 +417,79 @@ __global__ void __launch_bounds__(MID_THREADS, MID_CTAS) mid_product(const MidPa
 }
 
 constexpr uint32_t IMAGE_WARPS = 8;
+constexpr uint32_t ROUTE_FEW = 4096;  // pairs up to which one CTA routes them
+
+struct RouteParams {
+    const uint32_t *ids;
+    uint32_t *offsets, *sorted_pairs, *tiles, *tile_count, *err;
+    uint32_t R, E;
+};
+
+// The pairs by expert and the tiles of each expert, by one CTA beside those that write the
+// images (three launches less). A pair's column is computed by itself, so the order of an
+// expert's pairs, which the atomics leave open, changes no result.
+__device__ void route_few(const RouteParams &P) {
+    __shared__ uint32_t at[ROUTE_MAX_E + 4], sums[IMAGE_WARPS];
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+    constexpr uint32_t T = 32 * IMAGE_WARPS, EACH = ROUTE_MAX_E / T;
+    for (uint32_t i = tid; i < ROUTE_MAX_E; i += T) at[i] = 0u;
+    __syncthreads();
+    for (uint32_t p = tid; p < P.R; p += T) {
+        const uint32_t id = __ldg(P.ids + p);
+        if (id < P.E) atomicAdd(&at[id], 1u);
+        else atomicOr(P.err, ERR_BAD_ID);
+    }
+    __syncthreads();
+    // pairs (at most 4,096) and tiles (at most 4,096 / 24 + 1,024) before each expert, in one word
+    uint32_t n[EACH], own = 0u;
+#pragma unroll
+    for (uint32_t i = 0; i < EACH; i++) {
+        n[i] = at[EACH * tid + i];
+        own += n[i] | ((n[i] + MID_PAIRS - 1u) / MID_PAIRS) << 16;
+    }
+    uint32_t sum = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_up_sync(FULL, sum, d);
+        if (lane >= (uint32_t)d) sum += o;
+    }
+    if (lane == 31u) sums[warp] = sum;
+    __syncthreads();
+    sum -= own;
+    for (uint32_t w = 0; w < warp; w++) sum += sums[w];
+#pragma unroll
+    for (uint32_t i = 0; i < EACH; i++) {
+        const uint32_t e = EACH * tid + i;
+        at[e] = sum & 0xFFFFu;
+        if (e <= P.E) P.offsets[e] = sum & 0xFFFFu;
+        for (uint32_t r0 = 0, t = sum >> 16; r0 < n[i]; r0 += MID_PAIRS, t++) {
+            P.tiles[2u * t] = e;
+            P.tiles[2u * t + 1u] = r0;
+        }
+        sum += n[i] | ((n[i] + MID_PAIRS - 1u) / MID_PAIRS) << 16;
+    }
+    if (tid == T - 1u) {
+        *P.tile_count = sum >> 16;
+        if (P.E == ROUTE_MAX_E) P.offsets[P.E] = sum & 0xFFFFu;
+    }
+    __syncthreads();
+    for (uint32_t p = tid; p < P.R; p += T) {
+        const uint32_t id = __ldg(P.ids + p);
+        if (id < P.E) P.sorted_pairs[atomicAdd(&at[id], 1u)] = p;
+    }
+}
+
 // The tokens' images, in the order of MODE's codes, and the power of two of each. A CTA a
 // token: the largest |value| first, so that the products need no factor for each unit.
+// With up to ROUTE_FEW pairs one more CTA routes them.
 template <int MODE>
-__global__ void __launch_bounds__(32 * IMAGE_WARPS) mid_images(const void *x, int dt, uint32_t k, uint8_t *img, float *tf) {
+__global__ void __launch_bounds__(32 * IMAGE_WARPS) mid_images(const void *x, int dt, uint32_t m, uint32_t k, uint8_t *img,
+                                                               float *tf, const RouteParams route) {
+    ptx::griddep_launch_dependents();
+    if (blockIdx.x == m) {
+        route_few(route);
+        return;
+    }
     __shared__ uint32_t most[IMAGE_WARPS];
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, steps = (k + 127u) / 128u;
     const size_t row = (size_t)blockIdx.x * k;
@@ -454,8 +529,18 @@ cudaError_t product(const MidParams &P, uint32_t max_tiles, cudaStream_t st) {
     static int smem_set[64];
     const cudaError_t e = ensure_dyn_smem(kern, smem, smem_set);
     if (e != cudaSuccess) return e;
-    kern<<<dim3((P.n * (UP ? 2u : 1u) + MID_ROWS - 1u) / MID_ROWS, max_tiles), MID_THREADS, smem, st>>>(P);
-    return cudaGetLastError();
+    // a programmatic dependent of the kernel before it, which saves the launch's latency
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((P.n * (UP ? 2u : 1u) + MID_ROWS - 1u) / MID_ROWS, max_tiles);
+    cfg.blockDim = dim3(MID_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, P);
 }
 
 template <bool UP>
@@ -479,7 +564,10 @@ uint32_t tiles_of(uint64_t R, uint32_t E) { return (uint32_t)(R / MID_PAIRS) + E
 
 }  // namespace
 
-// Pairs of up to MOE_MLP_MID_PAIRS an expert.
+// Up to MOE_MLP_MID_PAIRS pairs an expert, 24 with 6-bit codes. Measured against the grouped
+// products with 128 experts of 2,816 x 704, us: 24 pairs an expert 329 / 559 (affine 4 bits),
+// 299 / 395 (NVFP4), 419 / 579 (3-bit codebook), 477 / 566 (6 bits); 32 pairs 414 / 568, 378 / 404,
+// 534 / 590, 605 / 577.
 static uint64_t mid_limit(uint32_t E) { return tmin<uint64_t>((uint64_t)MOE_MLP_MID_PAIRS * E, 1u << 20); }
 
 uint64_t mlp_mid_workspace(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t S, uint32_t E) {
@@ -490,9 +578,10 @@ uint64_t mlp_mid_workspace(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t
 
 bool mlp_mid_supported(const MlpArgs &a) {
     const uint64_t R = (uint64_t)a.m * a.S;
+    const int m1 = mode_of(*a.gate_up, a.hidden), m2 = mode_of(*a.down, a.inter);
     // (images are addressed by 32 bits in steps of 16 bytes)
     return R <= mid_limit(a.E) && R * ((tmax(a.hidden, a.inter) + 127ull) / 128u) * (step_bytes(1) / 16u) < 1ull << 32 && a.E <= MOE_ROUTE_MAX_EXPERTS && a.x_dtype != DT_F32 && a.out_dtype != DT_F32 &&
-           mode_of(*a.gate_up, a.hidden) >= 0 && mode_of(*a.down, a.inter) >= 0 && ((uintptr_t)a.x & 7u) == 0;
+           m1 >= 0 && m2 >= 0 && (R <= 24ull * a.E || (m1 != M_A6 && m2 != M_A6)) && ((uintptr_t)a.x & 7u) == 0;
 }
 
 cudaError_t launch_mlp_mid(const MlpArgs &a, uint8_t *ws, uint8_t *own, cudaStream_t st) {
@@ -500,19 +589,21 @@ cudaError_t launch_mlp_mid(const MlpArgs &a, uint8_t *ws, uint8_t *own, cudaStre
     WsLayout L;
     if (!ws_layout(R, a.E, &L)) return cudaErrorInvalidValue;
     uint32_t *const err = (uint32_t *)(ws + L.err), *const tc = (uint32_t *)(ws + L.tile_count);
-    uint32_t *const counts = (uint32_t *)(ws + L.counts), *const offsets = (uint32_t *)(ws + L.offsets);
+    uint32_t *const offsets = (uint32_t *)(ws + L.offsets);
     uint32_t *const sp = (uint32_t *)(ws + L.sorted_pairs), *const tiles = (uint32_t *)own;
     uint8_t *const xi = own + al256(8ull * max_tiles), *const hi = xi + images(a.m, a.hidden);
     float *const tf = (float *)(hi + images(R, a.inter)), *const z = tf + al256(4ull * a.m) / 4u;
-    cudaError_t e = launch_route(a.ids, R, a.E, MID_PAIRS, counts, offsets, sp, tiles, tc, max_tiles,
-                                 (uint32_t *)(ws + L.chunk_hist), (uint32_t *)(ws + L.chunk_base), L.chunks, err, nullptr,
-                                 0, 0, st);
+    cudaError_t e = cudaSuccess;
+    const bool one = R <= ROUTE_FEW;
+    if (!one)
+        e = launch_route(a.ids, R, a.E, MID_PAIRS, (uint32_t *)(ws + L.counts), offsets, sp, tiles, tc, max_tiles,
+                         (uint32_t *)(ws + L.chunk_hist), (uint32_t *)(ws + L.chunk_base), L.chunks, err, nullptr, 0, 0, st);
     if (e != cudaSuccess) return e;
     const int m1 = mode_of(*a.gate_up, a.hidden), m2 = mode_of(*a.down, a.inter);
-    if (order_of(m1) == 1) mid_images<M_A4><<<a.m, 32 * IMAGE_WARPS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi, tf);
-    else if (order_of(m1) == 2) mid_images<M_A8><<<a.m, 32 * IMAGE_WARPS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi, tf);
-    else if (m1 == M_A6) mid_images<M_A6><<<a.m, 32 * IMAGE_WARPS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi, tf);
-    else mid_images<M_NV><<<a.m, 32 * IMAGE_WARPS, 0, st>>>(a.x, a.x_dtype, a.hidden, xi, tf);
+    auto images_of = order_of(m1) == 1 ? mid_images<M_A4> : order_of(m1) == 2 ? mid_images<M_A8>
+                   : m1 == M_A6 ? mid_images<M_A6> : mid_images<M_NV>;
+    images_of<<<a.m + (one ? 1u : 0u), 32 * IMAGE_WARPS, 0, st>>>(a.x, a.x_dtype, a.m, a.hidden, xi, tf,
+                                                                  RouteParams{a.ids, offsets, sp, tiles, tc, err, R, a.E});
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
     MidParams P{};
