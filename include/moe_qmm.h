@@ -392,19 +392,26 @@ typedef struct {
  *             device error word that moe_qmm_id_poll_error reads and clears. Calls
  *             that share it must be ordered on the GPU.
  *   path      MOE_PATH_AUTO, or MOE_PATH_DECODE (the few-token kernels wherever they
- *             apply) or MOE_PATH_GROUPED (never those). No launch flags.
- * The two products' formats may differ. Few tokens (at most MOE_MLP_FEW_TOKENS, with
- * at most MOE_MLP_FEW_PAIRS pairs; under AUTO at most 64 pairs or 4 an expert) take
- * two kernels, the second of which sums over the slots, where hidden and inter are
- * multiples of 32, affine and codebook groups powers of two >= 32, and packed,
- * scales, aux (affine) and x are 16-byte aligned. Otherwise moe_qmm_id_glu's and
- * moe_qmm_id's paths run (with MOE_PATH_AUTO, DECODE or GROUPED as given), then
- * moe_combine's kernel.
- * h has 11 significant bits in the few-token kernels for a bf16 result and 22
- * otherwise, under a power of two for each 32 values; elsewhere it is bf16 for bf16 x
- * and f32 for f16 and f32 x. The products and the sum are accumulated in f32 and out
- * is rounded once. A value of x or h that is not finite makes the results that it
- * enters not finite. Errors as moe_qmm_id_glu and moe_combine.
+ *             apply) or MOE_PATH_GROUPED (the products of moe_qmm_id). No launch flags.
+ * The two products' formats may differ. Three ways, the first two where hidden and inter
+ * are multiples of 32, affine and codebook groups powers of two >= 32, and packed, scales
+ * and aux (affine) are 16-byte aligned:
+ *   few tokens (at most MOE_MLP_FEW_TOKENS, with at most MOE_MLP_FEW_PAIRS pairs, x 16-byte
+ *     aligned): two kernels, the second of which sums over the slots. AUTO takes them up
+ *     to 16 pairs or 1 an expert (1/4 where a product's codes are not affine, NVFP4 or
+ *     MXFP4 of 4 bits), or with an f32 type up to 64 pairs or 4 an expert;
+ *   up to MOE_MLP_MID_PAIRS pairs an expert (24 with 6-bit codes), x and out of 16 bits, x
+ *     8-byte aligned (AUTO only): grouped products over tiles of 24 pairs, then
+ *     moe_combine's kernel;
+ *   otherwise moe_qmm_id_glu's and moe_qmm_id's paths (with MOE_PATH_AUTO, DECODE or
+ *     GROUPED as given), then moe_combine's kernel.
+ * h has 11 significant bits, under a power of two for each 32 values, in the first two
+ * ways for a 16-bit result (22 in the few-token kernels for f16); 22 for an f32 result;
+ * in the last way it is bf16 for bf16 x and f32 otherwise. The second way scales x by one
+ * power of two a token: values below 2^-39 of its largest count as 0. The products and
+ * the sum are accumulated in f32 and out is rounded once. A value of x or h that is not
+ * finite makes the results that it enters not finite. Errors as moe_qmm_id_glu and
+ * moe_combine.
  */
 #define MOE_MLP_FEW_TOKENS 64u
 #define MOE_MLP_FEW_PAIRS 512u

@@ -1,9 +1,11 @@
 // mlp.cu -- the gated expert MLP of a layer (include/moe_qmm.h, moe_mlp):
 //   h[t][s]  = act(G_e x_t) * (U_e x_t),        e = ids[t][s]
 //   out[t]   = residual[t] + sum_s weights[t][s] * (D_e h[t][s])
-// Two ways, chosen by size:
+// Three ways, chosen by size:
 //   few tokens   the two kernels of mlp_few.cu (the sum over the slots happens in
 //                the down projection's kernel);
+//   up to some tens of pairs an expert, 16-bit types
+//                the grouped products of mlp_mid.cu and the weighted sum;
 //   otherwise    the fused gate+up product, the down product over the pairs and the
 //                weighted sum, each a call of this library.
 #include "common.cuh"
@@ -93,18 +95,20 @@ moe_status moe_mlp(const void *x, const uint32_t *ids, const float *weights, con
     const MlpArgs a{x,      ids,   weights, gate_up,       down,        residual,     out,           m,
                     hidden, inter, n_expert_used, num_experts, (int)x_dtype, (int)out_dtype, (int)act};
     // The few-token kernels have four pairs' worth of tensor work for one and no routing;
-    // mlp_mid.cu's products read and expand an expert's weights once for 24 pairs after it.
-    // Measured with 2,816 x 704 experts, few against mid, us: 256 experts, half a pair an
-    // expert 101 / 151 (affine 4 bits), 103 / 131 (NVFP4), 204 / 207 (3-bit codebook), 222 / 170
-    // (affine 8 bits); 1 pair 184 / 218, 193 / 191, 379 / 312, 392 / 248; 2 pairs 289 / 286, 311 /
-    // 250, 534 / 415, 604 / 324. 8 experts: 16 pairs in all 23 / 40, 38 / 50 (codebook), 32 pairs
-    // 42 / 43, 48 / 51, 64 pairs 61 / 46, 70 / 56. Where mlp_mid.cu does not apply (32-bit types),
-    // few against grouped: 4 pairs an expert 110 / 177, 116 / 128, 147 / 180 (affine 8 bits),
-    // 8 171 / 179, 179 / 131, 268 / 183; 64 pairs of 8 experts 49 / 79, 52 / 63, 66 / 83.
+    // mlp_mid.cu's products route first, then read and expand an expert's weights once for 24
+    // pairs, and gain the more, the longer that takes. Few against mid, 2,816 x 704
+    // experts, us: 256 experts at 1/2 pair an expert 101 / 135 (affine 4 bits), 103 / 116 (NVFP4),
+    // 204 / 192 (3-bit codebook), 221 / 157 (affine 8 bits); at 1 pair 184 / 199, 193 / 172, 376 /
+    // 292, 391 / 232; at 2 pairs 288 / 261, 313 / 227, 531 / 390, 604 / 306. Of 8 experts, 16 pairs
+    // in all 23 / 33, 23 / 29, 38 / 40, 40 / 39; 32 pairs 40 / 34, 42 / 32, 48 / 40, 53 / 40.
+    // Where mlp_mid.cu does not apply (32-bit types) the grouped products are left: few
+    // against grouped, 16-bit types, at 4 pairs an expert 110 / 177 (affine 4 bits), 116 / 128
+    // (NVFP4), 147 / 180 (affine 8 bits), at 8 171 / 179, 179 / 131, 268 / 183; 64 pairs of 8
+    // experts 49 / 79, 52 / 63, 66 / 83.
     const bool mid = path == MOE_PATH_AUTO && mlp_mid_supported(a);
     auto narrow = [](const moe_expert_weights *w) { return w->bits == 4 && w->fmt != MOE_FMT_CODEBOOK; };
     const uint64_t few_to = !mid ? tmax<uint64_t>(64u, 4ull * num_experts)
-                                   : tmax<uint64_t>(32u, narrow(gate_up) && narrow(down) ? num_experts : num_experts / 2u);
+                                 : tmax<uint64_t>(16u, narrow(gate_up) && narrow(down) ? num_experts : num_experts / 4u);
     if (path != MOE_PATH_GROUPED && (path == MOE_PATH_DECODE || R <= few_to) && mlp_few_supported(a))
         return launch_mlp_few(a, (uint32_t *)ws, h, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     if (mid) return launch_mlp_mid(a, ws, ws + L.h, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
