@@ -26,7 +26,7 @@
 // to expand and scale the codes, 20 for each block of 8 pairs, 30 for copies and scales; the
 // scheduler issues in 57 % of its cycles, the ALU is busy for 46 %, MMA for 21 %.
 // 128 experts of 2,816 x 704, top-8, 256 tokens: 288 us (3-bit codebook; the tcgen05 grouped
-// products 568), 225 (affine 4 bits; 553), 205 (NVFP4; 391), 245 (affine 8 bits; 560).
+// products 568), 224 (affine 4 bits; 553), 203 (NVFP4; 391), 248 (affine 8 bits; 560).
 #include "common.cuh"
 #include "internal.h"
 #include "mlp_codes.cuh"

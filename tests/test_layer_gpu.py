@@ -436,6 +436,68 @@ def test_two_layers_on_two_streams():
         assert all(torch.equal(o, outs[i][0]) for o in outs[i])
 
 
+@pytest.mark.parametrize("m,E,k", [(700, 256, 8), (300, 1024, 8), (128, 4, 1), (129, 4, 1), (90, 1, 1)])
+def test_mlp_many_experts_and_pairs(m, E, k):
+    """More pairs than one CTA routes, the most experts, the last size of tens of pairs an
+    expert and the first of the next way, one expert."""
+    L = LR.Layer(m=m, hidden=64, inter=32, top_k=k, E=E, fmt=FMT_AFFINE, bits=4, gs=32, x_dtype=DT_BF16, seed=m)
+    layer = build(L, out_dtype=DT_BF16, max_tokens=m + 200)
+    out = layer(*inputs(L))
+    check(L, out, DT_BF16)
+    assert torch.equal(out, layer(*inputs(L)))
+
+
+def test_layers_of_tens_of_pairs_overlap_and_replay():
+    """Two layers on two streams, eager and captured at once, one of them also at fewer
+    tokens in between: the same results as alone."""
+    Ls = [LR.Layer(m=48, hidden=256, inter=160, top_k=4, E=8, fmt=f, bits=b, gs=g, x_dtype=DT_BF16, seed=30 + b)
+          for f, b, g in ((FMT_AFFINE, 8, 32), (FMT_CODEBOOK, 3, 32))]
+    layers = [build(L, out_dtype=DT_BF16) for L in Ls]
+    ins = [inputs(L) for L in Ls]
+    want = [layer(*i) for layer, i in zip(layers, ins)]
+    few = layers[0](ins[0][0][:2], ins[0][1][:2], ins[0][2][:2])
+    for L, w in zip(Ls, want):
+        check(L, w, DT_BF16)
+    graphs, gout = [], []
+    for layer, i in zip(layers, ins):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            gout.append(layer(*i))
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in Ls]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):
+        for n, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs.append((want[n], layers[n](*ins[n])))
+                if n == 0:
+                    outs.append((few, layers[0](ins[0][0][:2], ins[0][1][:2], ins[0][2][:2])))
+                gout[n].zero_()
+                graphs[n].replay()
+                outs.append((want[n], gout[n].clone()))
+    torch.cuda.synchronize()
+    assert all(torch.equal(w, o) for w, o in outs)
+
+
+def test_mlp_tens_of_pairs_rows_do_not_mix():
+    """A token with NaN, one with infinities and one without an expert leave the other
+    tokens' results alone."""
+    L = LR.Layer(m=40, hidden=256, inter=128, top_k=2, E=4, fmt=FMT_AFFINE, bits=4, gs=32, x_dtype=DT_BF16, seed=12)
+    layer = build(L, out_dtype=DT_BF16)
+    x, ids, w = inputs(L)
+    want = layer(x, ids, w)
+    x2, ids2 = x.clone(), ids.clone()
+    x2[3] = float("nan")
+    x2[17, 5] = float("inf")
+    ids2[30] = 4
+    out = layer(x2, ids2, w)
+    keep = [t for t in range(40) if t not in (3, 17, 30)]
+    assert torch.equal(out[keep], want[keep])
+    assert out[3].isnan().all() and not out[17].isfinite().any()
+    assert torch.count_nonzero(out[30]) == 0 and M.poll_error(layer.workspace) != 0
+
+
 def test_mlp_refusals():
     L = LR.Layer(m=3, hidden=128, inter=64, top_k=2, E=4, fmt=FMT_AFFINE, bits=4, gs=32, x_dtype=DT_BF16, seed=8)
     layer = build(L, out_dtype=DT_BF16)
