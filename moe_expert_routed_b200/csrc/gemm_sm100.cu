@@ -1044,17 +1044,20 @@ grouped_gemm_kernel(const GemmParams P, const __grid_constant__ CUtensorMap tmap
             if (!load_item(w)) continue;
             const uint32_t buf = done % NACC, use = done / NACC;
             const uint32_t *pairs = P.sorted_pairs + it.off + it.r0;
-            // lane j < 16 fetches column c0 + j's pair and its token's factor, a chunk ahead of
-            // their use and the first before the accumulator is ready: two dependent loads
-            // from L2 a chunk would otherwise outlast the mainloop of a short k
+            // lane j < 16 fetches column c0 + j's pair and its token's factor. With 256-pair tiles
+            // a chunk ahead of their use and the first before the accumulator is ready: two
+            // dependent loads from L2 a chunk would otherwise outlast the mainloop of a short k
+            // (prefill's down product 711 -> 587 us). Tiles of few chunks have their results
+            // later for it (canvas 305 -> 312 us).
+            constexpr bool AHEAD = BN == 256;
             auto fetch = [&](uint32_t c0, uint32_t &p, float &f) {
                 const uint32_t cj = c0 + (lane & 15u);
                 p = cj < it.nt ? __ldg(pairs + cj) : 0u;
                 f = P.tok_scale ? __ldg(P.tok_scale + p / P.n_expert_used) : 1.f;
             };
-            uint32_t nextp;
-            float nextf;
-            fetch(0u, nextp, nextf);
+            uint32_t nextp = 0u;
+            float nextf = 1.f;
+            if constexpr (AHEAD) fetch(0u, nextp, nextf);
             if (!ptx::mbar_wait_bounded(accfull0 + 8 * buf, use & 1u, abort_flag, P.err, ERR_TIMEOUT, P.timeout_ns))
                 break;
             ptx::tc_fence_after();
@@ -1067,9 +1070,10 @@ grouped_gemm_kernel(const GemmParams P, const __grid_constant__ CUtensorMap tmap
             for (uint32_t c0 = 0; c0 < it.nt; c0 += 16) {
                 uint32_t v[16], pr[16];
                 ptx::tmem_ld16(d + ((q * 32u) << 16) + c0, v);
+                if constexpr (!AHEAD) fetch(c0, nextp, nextf);
                 const uint32_t myp = nextp;
                 const float myf = nextf;
-                if (c0 + 16u < it.nt) fetch(c0 + 16u, nextp, nextf);
+                if (AHEAD && c0 + 16u < it.nt) fetch(c0 + 16u, nextp, nextf);
 #pragma unroll
                 for (int i = 0; i < 16; i++) pr[i] = __shfl_sync(0xFFFFFFFFu, myp, i);
                 ptx::tmem_wait_ld();
