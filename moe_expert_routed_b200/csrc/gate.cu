@@ -10,7 +10,10 @@
 // Softmax and sigmoid are monotonic, so without a selection bias the choice is made
 // on the logits themselves and is exact. With a bias the choice is by sigmoid(l) + b:
 // two experts can then lie closer than a 32-bit sigmoid tells apart, so that sum is
-// formed in 64 bits and compared as a 64-bit key (two redux rounds).
+// formed in 64 bits and compared as a 64-bit key (two redux rounds). The 64-bit
+// exponentials would bound it (8,192 x 256: 23 us against 17), so they are taken only of the
+// experts that a 32-bit score with its error bound cannot rule out: as a rule the k
+// chosen and few more, one a lane.
 #include "common.cuh"
 #include "internal.h"
 
@@ -43,20 +46,10 @@ struct GateParams {
     float scale;
 };
 
-// V: logits per lane (E <= 32 V). BIAS: sigmoid scores chosen with a selection bias.
+// The choice among all experts: lane r's my_e is the r-th.
 template <int V, bool BIAS>
-__global__ void __launch_bounds__(GATE_WARPS * 32) gate_topk(const GateParams P) {
-    const uint32_t lane = threadIdx.x & 31u;
-    const uint64_t t = (uint64_t)blockIdx.x * GATE_WARPS + (threadIdx.x >> 5);
-    if (t >= P.m) return;
-    const size_t row = t * P.E;
-    float l[V];
+__device__ __forceinline__ void choose(const GateParams &P, const float (&l)[V], uint32_t lane, uint32_t &my_e) {
     uint32_t hi[V], lo[BIAS ? V : 1];
-#pragma unroll
-    for (int j = 0; j < V; j++) {
-        const uint32_t e = j * 32u + lane;
-        l[j] = e < P.E ? load_x(P.logits, P.dtype, row + e) : 0.f;
-    }
 #pragma unroll
     for (int j = 0; j < V; j++) {
         const uint32_t e = j * 32u + lane;
@@ -71,7 +64,6 @@ __global__ void __launch_bounds__(GATE_WARPS * 32) gate_topk(const GateParams P)
     }
 
     // rounds: lane r keeps the r-th choice (k <= 32 and k <= E: a key above 0 is left)
-    uint32_t my_e = 0;
     for (uint32_t r = 0; r < P.k; r++) {
         uint32_t top = 0, low = 0;
         if constexpr (BIAS) {
@@ -103,6 +95,88 @@ __global__ void __launch_bounds__(GATE_WARPS * 32) gate_topk(const GateParams P)
             }
         if (lane == r) my_e = e;
     }
+}
+
+// The same with a selection bias, among the experts whose 32-bit score may reach the k-th:
+// false if there are more than 32 of those. The score is off by less than 2^-21: of the
+// sigmoid s, s (1 - s) (2 + 1.16 |l|) 2^-23 < 2^-24 by __expf, 2^-24 by the sum, 2^-22 by
+// __fdividef (2 units in the last place); and 2^-24 of the sum with the bias. Twice
+// that is allowed for. An expert among the k best scores no less than the k-th largest lower
+// bound, so its upper bound does not lie below that.
+template <int V>
+__device__ __forceinline__ bool choose_few(const GateParams &P, const float (&l)[V], size_t row, uint32_t *few,
+                                           uint32_t lane, uint32_t &my_e) {
+    float v[V];
+    uint32_t low[V];
+#pragma unroll
+    for (int j = 0; j < V; j++) {
+        const uint32_t e = j * 32u + lane;
+        v[j] = e < P.E ? __fdividef(1.f, 1.f + __expf(-l[j])) + __ldg(P.bias + e) : 0.f;
+        const float d = isinf(v[j]) ? 0.f : fmaf(fabsf(v[j]), 0x1p-23f, 0x1p-20f);
+        low[j] = e < P.E ? key32(v[j] - d) : 0u;
+    }
+    uint32_t cut = 0, n = 0;
+    while (n < P.k) {  // takes away all that are as large as the largest left; k <= E
+        uint32_t top = 0, same = 0;
+#pragma unroll
+        for (int j = 0; j < V; j++) top = max(top, low[j]);
+        cut = __reduce_max_sync(FULL, top);
+#pragma unroll
+        for (int j = 0; j < V; j++)
+            if (low[j] == cut) low[j] = 0u, same++;
+        n += __reduce_add_sync(FULL, same);
+    }
+    uint32_t c = 0;
+#pragma unroll
+    for (int j = 0; j < V; j++) {
+        const uint32_t e = j * 32u + lane;
+        const float d = isinf(v[j]) ? 0.f : fmaf(fabsf(v[j]), 0x1p-23f, 0x1p-20f);
+        const bool in = e < P.E && key32(v[j] + d) >= cut;
+        const uint32_t who = __ballot_sync(FULL, in), at = c + __popc(who & ((1u << lane) - 1u));
+        if (in && at < 32u) few[at] = e;
+        c += __popc(who);
+    }
+    if (c > 32u) return false;
+    __syncwarp();
+    // one a lane, by expert
+    uint32_t hi = 0u, lo = 0u, mine = 0u;
+    if (lane < c) {
+        mine = few[lane];
+        const float x = load_x(P.logits, P.dtype, row + mine);
+        const uint64_t key = key64(1.0 / (1.0 + exp(-(double)x)) + (double)__ldg(P.bias + mine));
+        hi = (uint32_t)(key >> 32);
+        lo = (uint32_t)key;
+    }
+    for (uint32_t r = 0; r < P.k; r++) {
+        const uint32_t top = __reduce_max_sync(FULL, hi), low32 = __reduce_max_sync(FULL, hi == top ? lo : 0u);
+        const uint32_t first = __ffs(__ballot_sync(FULL, lane < c && hi == top && lo == low32)) - 1u;
+        const uint32_t e = __shfl_sync(FULL, mine, first);
+        if (lane == r) my_e = e;
+        if (lane == first) hi = lo = 0u;
+    }
+    return true;
+}
+
+// V: logits per lane (E <= 32 V). BIAS: sigmoid scores chosen with a selection bias.
+template <int V, bool BIAS>
+__global__ void __launch_bounds__(GATE_WARPS * 32) gate_topk(const GateParams P) {
+    const uint32_t lane = threadIdx.x & 31u;
+    const uint64_t t = (uint64_t)blockIdx.x * GATE_WARPS + (threadIdx.x >> 5);
+    if (t >= P.m) return;
+    const size_t row = t * P.E;
+    float l[V];
+#pragma unroll
+    for (int j = 0; j < V; j++) {
+        const uint32_t e = j * 32u + lane;
+        l[j] = e < P.E ? load_x(P.logits, P.dtype, row + e) : 0.f;
+    }
+    uint32_t my_e = 0;
+    bool done = false;
+    if constexpr (BIAS) {
+        __shared__ uint32_t few[GATE_WARPS][32];
+        done = choose_few<V>(P, l, row, few[threadIdx.x >> 5], lane, my_e);
+    }
+    if (!done) choose<V, BIAS>(P, l, lane, my_e);
 
     // weights of the chosen
     const bool mine = lane < P.k;

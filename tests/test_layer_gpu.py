@@ -55,6 +55,27 @@ def test_gate_ties_go_to_the_lowest_expert():
     assert np.array_equal(ids.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("near", [1, 12, 40, 300])
+def test_gate_selection_bias_decided_in_64_bits(near):
+    """Scores that 32 bits cannot tell apart, a few of them and more than a warp holds, at
+    the cut and above it; selection biases that are large, infinite and NaN."""
+    rng = np.random.default_rng(near)
+    m, E, k = 9, 400, 10
+    l = rng.standard_normal((m, E)).astype(np.float32)
+    b = (rng.standard_normal(E) * 0.1).astype(np.float32)
+    for t in range(m):
+        at = rng.permutation(E)[:near]
+        l[t, at] = 18 + rng.permutation(near) * 2.0**-7  # sigmoid within 2^-26 of 1
+        b[at] = 1.0
+    b[:4] = [1e6, -1e6, np.inf, -np.inf]
+    ids, _ = M.gate_topk(torch.from_numpy(l).cuda(), k, score="sigmoid", select_bias=torch.from_numpy(b).cuda())
+    assert np.array_equal(ids.cpu().numpy(), LR.gate(l, k, "sigmoid", b)[0])
+    b[5] = np.nan
+    ids, _ = M.gate_topk(torch.from_numpy(l).cuda(), k, score="sigmoid", select_bias=torch.from_numpy(b).cuda())
+    b[5] = -np.inf  # NaN below every number, and no -inf among the first k
+    assert np.array_equal(ids.cpu().numpy(), LR.gate(l, k, "sigmoid", b)[0])
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_gate_masked_and_non_finite_logits(score):
     inf, nan = float("inf"), float("nan")
