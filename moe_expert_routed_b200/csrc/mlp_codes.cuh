@@ -187,21 +187,21 @@ __device__ __forceinline__ void expand(const uint32_t (&w)[words(MODE)], int t, 
             : "=r"(p[0]), "=r"(p[1]), "=r"(p[2]), "=r"(p[3])
             : "r"(w[t]));
     } else {
-        // the codes spread to nibbles: halves, quarters and eighths apart
+        // the codes spread to nibbles: halves, quarters and eighths apart, other bits last
         uint32_t n;
         if constexpr (MODE == M_CB4) {
             n = w[t];
         } else if constexpr (MODE == M_CB2) {
             const uint32_t v = t & 1 ? w[t / 2] >> 16 : w[t / 2];
-            n = (v & 0xFFu) | ((v << 8) & 0x00FF0000u);
-            n = (n & 0x000F000Fu) | ((n << 4) & 0x0F000F00u);
-            n = (n & 0x03030303u) | ((n << 2) & 0x30303030u);
+            n = (v & 0xFFu) | ((v << 8) & ~0xFFu);
+            n = (n & 0x00FF00FFu) | ((n << 4) & 0xFF00FF00u);
+            n = ((n & 0x0F0F0F0Fu) | ((n << 2) & 0xF0F0F0F0u)) & 0x33333333u;
         } else {
             const uint32_t v = t == 0 ? w[0] : t == 1 ? __funnelshift_r(w[0], w[1], 24)
                              : t == 2 ? __funnelshift_r(w[1], w[2], 16) : w[2] >> 8;
-            n = (v & 0xFFFu) | ((v << 4) & 0x0FFF0000u);
-            n = (n & 0x003F003Fu) | ((n << 2) & 0x3F003F00u);
-            n = (n & 0x07070707u) | ((n << 1) & 0x70707070u);
+            n = (v & 0xFFFu) | ((v << 4) & ~0xFFFu);
+            n = (n & 0x00FF00FFu) | ((n << 2) & 0xFF00FF00u);
+            n = ((n & 0x0F0F0F0Fu) | ((n << 1) & 0xF0F0F0F0u)) & 0x77777777u;
         }
         T.look(n, p[0], p[1]);
         T.look(n >> 16, p[2], p[3]);

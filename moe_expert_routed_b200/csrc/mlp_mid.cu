@@ -116,9 +116,9 @@ __device__ __forceinline__ void quarter(uint32_t at, uint32_t u, uint32_t q, uin
     } else if constexpr (MODE == M_CB2) {
         w[0] = lds16(at + u * 8u + q * 2u);
     } else if constexpr (MODE == M_CB3) {
-        const uint32_t word = code * 205u >> 11, m = 0x3FFFFFFFu;  // code / 10 (codes below 138)
-        const uint32_t a = lds32(at + word * 4u) & m, b = lds32(at + word * 4u + 4u) & m;
-        w[0] = __funnelshift_r(a | (b << 30), b >> 2, 3u * (code - 10u * word));
+        const uint32_t word = code * 205u >> 11;  // code / 10 (codes below 138)
+        // 30 bits of the first word, then the next one's
+        w[0] = __funnelshift_r(lds32(at + word * 4u) << 2, lds32(at + word * 4u + 4u), 3u * (code - 10u * word) + 2u);
     } else {
         w[0] = lds32(at + u * 16u + q * 4u);
     }
