@@ -22,11 +22,11 @@
 // one barrier a step. Eight warps a CTA, two CTAs an SM: 338 us against 322 (256 tokens,
 // 3-bit codebook), 264 against 238 (NVFP4). 24 pairs a tile leave the registers for five
 // CTAs: 242 us against 260 with tiles of 32 and four (affine 4 bits), 221 against 232.
-// Bound by instructions: for each unit and 32 rows 40 (affine 4 bits) to 110 (3-bit codebook)
+// Bound by instructions: for each unit and 32 rows 40 (affine 4 bits) to 90 (3-bit codebook)
 // to expand and scale the codes, 20 for each block of 8 pairs, 30 for copies and scales; the
 // scheduler issues in 57 % of its cycles, the ALU is busy for 46 %, MMA for 21 %.
-// 128 experts of 2,816 x 704, top-8, 256 tokens: 288 us (3-bit codebook; the tcgen05 grouped
-// products 568), 224 (affine 4 bits; 553), 203 (NVFP4; 391), 248 (affine 8 bits; 560).
+// 128 experts of 2,816 x 704, top-8, 256 tokens: 278 us (3-bit codebook; the tcgen05 grouped
+// products 558), 224 (affine 4 bits; 554), 202 (NVFP4; 389), 247 (affine 8 bits; 561).
 #include "common.cuh"
 #include "internal.h"
 #include "mlp_codes.cuh"
