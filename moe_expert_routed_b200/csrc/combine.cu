@@ -18,7 +18,7 @@ constexpr int COMBINE_THREADS = 256;
 
 struct CombineParams {
     const void *z;
-    const float *w;
+    const float *w;  // null: 1 (rows that carry their weights)
     const uint32_t *ids;
     const void *residual;
     void *out;
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(const CombineP
             for (int k = 0; k < B; k++) v[k] = load_once(z + (size_t)k * nv);
 #pragma unroll
             for (int k = 0; k < B; k++) {
-                const float ws = __ldg(w + s0 + k);
+                const float ws = P.w ? __ldg(w + s0 + k) : 1.f;
 #pragma unroll
                 for (int j = 0; j < VEC; j++) acc[j] = fmaf(ws, Cvt<TZ>::to(v[k].v[j]), acc[j]);
             }
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(const CombineP
     } else {
         for (uint32_t s = 0; s < P.S; s++) {
             if (P.ids && __ldg(P.ids + (size_t)t * P.S + s) >= P.E) continue;  // not read
-            const float ws = __ldg(w + s);
+            const float ws = P.w ? __ldg(w + s) : 1.f;
             const Pack<TZ, VEC> v = load_once(z + (size_t)s * nv);
 #pragma unroll
             for (int j = 0; j < VEC; j++) acc[j] = fmaf(ws, Cvt<TZ>::to(v.v[j]), acc[j]);

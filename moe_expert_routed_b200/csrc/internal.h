@@ -127,7 +127,8 @@ cudaError_t launch_gemm(const QmmArgs &a, const uint32_t *offsets, const uint32_
                         uint32_t *err, uint32_t *work_counter, const uint16_t *xg, const uint8_t *ximg,
                         cudaStream_t st);
 
-// out[t] = residual[t] + sum_s weights[t][s] * z[t][s] (moe_combine without its checks).
+// out[t] = residual[t] + sum_s weights[t][s] * z[t][s] (moe_combine without its checks;
+// weights null: 1).
 cudaError_t launch_combine(const void *z, const float *weights, const uint32_t *ids, const void *residual, void *out,
                            uint32_t m, uint32_t S, uint32_t n, uint32_t E, int z_dtype, int out_dtype,
                            cudaStream_t st);

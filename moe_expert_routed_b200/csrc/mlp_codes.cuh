@@ -221,7 +221,8 @@ __device__ __forceinline__ void expand(const uint32_t (&w)[words(MODE)], int t, 
 }
 constexpr bool centred(int mode, int planes) { return affine(mode) && planes == 2; }
 constexpr float middle(int mode) { return mode == M_A8 ? 128.f : mode == M_A6 ? 32.f : 8.f; }
-// What expand()'s values have to be multiplied by.
+// What expand()'s values have to be multiplied by: the sums of x that meet the biases are
+// divided by it and the results multiplied, since a unit's factor times 2^24 can leave f32.
 constexpr float code_unit(int mode, int planes) { return affine(mode) && !centred(mode, planes) ? 16777216.f : 1.f; }
 
 // Order of x against expand()'s pairs: 0 as it stands, 1 as 4-bit affine words part it

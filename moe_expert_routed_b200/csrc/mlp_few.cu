@@ -180,7 +180,8 @@ __device__ __forceinline__ void step(uint32_t st, uint32_t sc, uint32_t tot, uin
     float f[NB][2], xs[NB][2];
     const bool odd_plane = PLANES == 2 && (lane & 2u);
     constexpr bool CENTRED = centred(MODE, PLANES);
-    const float unit = odd_plane ? code_unit(MODE, PLANES) * 4.8828125e-4f : code_unit(MODE, PLANES);  // 2^-11
+    const float plane = odd_plane ? 4.8828125e-4f : 1.f;  // 2^-11
+    constexpr float unit = 1.f / code_unit(MODE, PLANES);
 #pragma unroll
     for (int n = 0; n < NB; n++) {
 #pragma unroll
@@ -189,10 +190,10 @@ __device__ __forceinline__ void step(uint32_t st, uint32_t sc, uint32_t tot, uin
             B[n][4 * k] = v.x; B[n][4 * k + 1] = v.y; B[n][4 * k + 2] = v.z; B[n][4 * k + 3] = v.w;
         }
         const uint4 v = lds128(at.f[n] + on);
-        f[n][0] = __uint_as_float(v.x) * unit;
-        f[n][1] = __uint_as_float(v.z) * unit;
-        xs[n][0] = odd_plane ? 0.f : __uint_as_float(v.y);  // the bias once a pair
-        xs[n][1] = odd_plane ? 0.f : __uint_as_float(v.w);
+        f[n][0] = PLANES == 2 ? __uint_as_float(v.x) * plane : __uint_as_float(v.x);
+        f[n][1] = PLANES == 2 ? __uint_as_float(v.z) * plane : __uint_as_float(v.z);
+        xs[n][0] = odd_plane ? 0.f : __uint_as_float(v.y) * unit;  // the bias once a pair
+        xs[n][1] = odd_plane ? 0.f : __uint_as_float(v.w) * unit;
     }
 #pragma unroll
     for (uint32_t t = 0; t < T; t++) {
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const Few
             weight = __ldg(P.weights + p_e);
             if (P.scale2_kind) weight *= __ldg((const float *)P.a2 + e);
         }
-        const float s2 = MODE == M_NV ? __ldg((const float *)P.a1 + e) : 1.f;
+        const float s2 = MODE == M_NV ? __ldg((const float *)P.a1 + e) : code_unit(MODE, PLANES);
         wait_groups<RING - 1>();  // the first unit's scales came with the first step
         __syncthreads();          // images, scales
 
@@ -716,6 +717,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_down(const F
                     for (int h = 0; h < 2; h++) {
                         v[t][h] = acc[t][n][h] + __shfl_xor_sync(FULL, acc[t][n][h], 1);
                         if constexpr (NPL == 2) v[t][h] += __shfl_xor_sync(FULL, v[t][h], 2);
+                        v[t][h] *= code_unit(MODE, NPL);
                         acc[t][n][h] = 0.f;
                     }
                 // one pair at a time: two of them may be one token's

@@ -2,8 +2,8 @@
 // tokens, a batch of sequences. Two grouped products on mma.sync over the routing's tiles
 // of up to 24 pairs,
 //   mid_product<UP>    h[p] = act(G_e x_t) * (U_e x_t)
-//   mid_product<DOWN>  z[p] = D_e h[p]
-// and the weighted sum of z.
+//   mid_product<DOWN>  z[p] = weight[p] * D_e h[p]
+// and the sum of z (weighted first: small weights keep z in f32's range where h is large).
 //
 // With so few columns a 128-row tcgen05 tile is bound by what hands it the dequantised
 // operand, stage by stage, not by its arithmetic; here codes go from shared memory to the
@@ -25,7 +25,7 @@
 // Bound by instructions: for each unit and 32 rows 40 (affine 4 bits) to 90 (3-bit codebook)
 // to expand and scale the codes, 20 for each block of 8 pairs, 30 for copies and scales; the
 // scheduler issues in 57 % of its cycles, the ALU is busy for 46 %, MMA for 21 %.
-// 128 experts of 2,816 x 704, top-8, 256 tokens: 278 us (3-bit codebook; the tcgen05 grouped
+// 128 experts of 2,816 x 704, top-8, 256 tokens: 282 us (3-bit codebook; the tcgen05 grouped
 // products 558), 224 (affine 4 bits; 554), 202 (NVFP4; 389), 247 (affine 8 bits; 561).
 #include "common.cuh"
 #include "internal.h"
@@ -65,6 +65,7 @@ struct MidParams {
     const void *bias;            // expert biases, or null
     const uint8_t *x;            // images: [token] (UP), [place among the sorted pairs] (DOWN)
     const float *factor;         // UP: of the tokens' values
+    const float *weights;        // DOWN: of the pairs
     const uint32_t *offsets, *sorted_pairs, *tiles, *tile_count;
     void *out;                   // UP: images of h by sorted place; DOWN: z [pair][n] f32
     uint32_t k, n, S;            // n: rows of out (UP: of gate, the up rows follow)
@@ -370,11 +371,13 @@ __global__ void __launch_bounds__(MID_THREADS, ctas(MODE)) mid_product(const Mid
             for (uint32_t k = 0; k < 2; k++) {
                 const uint32_t pr = 8u * n + 2u * q + k;
                 if (pr < np) {
-                    float *const to = z + (size_t)P.sorted_pairs[place + pr] * P.n + row0 + r;
+                    const uint32_t pair = P.sorted_pairs[place + pr];
+                    const float wt = __ldg(P.weights + pair);
+                    float *const to = z + (size_t)pair * P.n + row0 + r;
 #pragma unroll
                     for (uint32_t i = 0; i < 4; i++) {
                         const float2 v = unpack2(acc[i >> 1][i & 1][n]);
-                        to[8u * i] = fmaf(k ? v.y : v.x, s2, bias[i]);
+                        to[8u * i] = fmaf(k ? v.y : v.x, s2 * wt, bias[i] * wt);
                     }
                 }
             }
@@ -630,13 +633,13 @@ cudaError_t launch_mlp_mid(const MlpArgs &a, uint8_t *ws, uint8_t *own, cudaStre
     if (e != cudaSuccess) return e;
     P.w = (const uint8_t *)a.down->packed; P.s = (const uint8_t *)a.down->scales;
     P.a = (const uint8_t *)a.down->aux; P.bias = a.down->bias; P.bias_dtype = (int)a.down->bias_dtype;
-    P.x = hi; P.out = z;
+    P.x = hi; P.out = z; P.weights = a.weights;
     P.k = a.inter; P.n = a.hidden;
     P.row_bytes = (uint32_t)moe_packed_row_bytes(a.down->fmt, a.down->bits, a.inter);
     P.groups = a.inter / a.down->group_size; P.gshift = log2_units(*a.down);
     e = product_m<false>(P, m2, max_tiles, st);
     if (e != cudaSuccess) return e;
-    return launch_combine(z, a.weights, a.ids, a.residual, a.out, a.m, a.S, a.hidden, a.E, DT_F32, a.out_dtype, st);
+    return launch_combine(z, nullptr, a.ids, a.residual, a.out, a.m, a.S, a.hidden, a.E, DT_F32, a.out_dtype, st);
 }
 
 }  // namespace moe

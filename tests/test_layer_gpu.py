@@ -275,6 +275,20 @@ def test_mlp_wide_range_of_x(x_dtype, m):
     check(L, layer(*inputs(L)), DT_F32)
 
 
+@pytest.mark.parametrize("fmt,most", [("aff4", 58), ("aff4g32", 58), ("aff6", 56), ("aff8", 54), ("nvfp4", 59),
+                                      ("cb3", 59)])
+@pytest.mark.parametrize("m", [2, 40])
+def test_mlp_huge_and_tiny_values(fmt, most, m):
+    """h up to about 2^120, and about 2^-85: the factors of its units stay in f32's range."""
+    f, bits, gs = FORMATS[fmt]
+    for scale in (2.0**most, 2.0**-45):
+        L = LR.Layer(m=m, hidden=256, inter=128, top_k=2, E=8, fmt=f, bits=bits, gs=gs, x_dtype=DT_BF16, seed=77)
+        x = torch.randn(m, 256, generator=torch.Generator().manual_seed(4), dtype=torch.float64) * scale
+        L.gu = L.gu.with_x(x.to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16))
+        L.w = (L.w * 2.0**-12).astype(np.float32)
+        check(L, build(L, out_dtype=DT_BF16)(*inputs(L)), DT_BF16)
+
+
 @pytest.mark.parametrize("x_dtype", [DT_BF16, DT_F16])
 @pytest.mark.parametrize("fmt", sorted(FORMATS))
 def test_mlp_tens_of_pairs_an_expert(fmt, x_dtype):
