@@ -27,6 +27,7 @@
 // scheduler issues in 57 % of its cycles, the ALU is busy for 46 %, MMA for 21 %.
 // 128 experts of 2,816 x 704, top-8, 256 tokens: 282 us (3-bit codebook; the tcgen05 grouped
 // products 558), 224 (affine 4 bits; 554), 202 (NVFP4; 389), 247 (affine 8 bits; 561).
+#include "cb3_blocks.h"
 #include "common.cuh"
 #include "internal.h"
 #include "mlp_codes.cuh"
@@ -267,13 +268,13 @@ __global__ void __launch_bounds__(MID_THREADS, ctas(MODE)) mid_product(const Mid
                     const uint8_t *g = w0 + ((i & 1u) * dr + (i >> 1) * dt) * P.row_bytes;
                     const uint32_t d = st + (warp * 32u + 8u * i + r) * LINE;
                     if constexpr (MODE == M_CB3) {
-                        const int word = (int)(128u * j / 10u), off = (int)(misplaced + word) & 3;
-                        auto block = [&](uint32_t k) {  // up to the row's end
-                            const int o = (word - off) * 4 + (int)k * 16, n = (int)P.row_bytes - o;
-                            ptx::cp_async_16(d + k * 16u, g + (n > 0 ? o : 0), n >= 16 ? 16u : n > 0 ? (uint32_t)n : 0u);
+                        auto block = [&](uint32_t k) {
+                            const Cb3Block c = cb3_block(misplaced, j, k, P.row_bytes);
+                            ptx::cp_async_16(d + k * 16u, g + c.at, c.bytes);
                         };
                         block(q);
-                        if (off == 3 && q == i) block(4u);  // 14 words from a block's fourth on: a fifth block
+                        // 14 words from a block's fourth on: a fifth block
+                        if (((misplaced + 128u * j / 10u) & 3u) == 3u && q == i) block(4u);
                     } else if constexpr (MODE == M_CB2) {
                         const uint32_t in = 4u * j + q < nu;
                         ptx::cp_async_8(d + q * 8u, g + (in ? (4u * j + q) * 8u : 0u), in ? 8u : 0u);
