@@ -338,8 +338,8 @@ typedef enum {
  *                the top_k chosen p where renormalize is non-zero.
  * The choice is by the logits without a bias (both scores are monotonic; exact),
  * and by p + bias in 64 bits with one. A logit of -inf masks its expert: it is
- * chosen after every other and has weight 0; a token whose logits are all -inf has
- * weights 0. A NaN logit ranks below -inf and makes the weights that it enters NaN,
+ * chosen after every other, whatever its bias, and has weight 0; a token whose
+ * logits are all -inf has weights 0. A NaN logit ranks below -inf and makes the weights that it enters NaN,
  * as a logit of +inf does under softmax.
  * MOE_ERR_INVALID_ARGUMENT: zero sizes, top_k > num_experts, unknown types, NULL
  * or misaligned arrays, a bias with softmax. MOE_ERR_UNSUPPORTED: num_experts >

@@ -24,7 +24,10 @@ namespace {
 constexpr int GATE_WARPS = 4;  // tokens per CTA
 constexpr uint32_t FULL = 0xFFFFFFFFu;
 
-// Keys: 0 retired or no expert, 1 NaN (below every number), else increasing with v.
+// Keys: 0 retired or no expert, 1 NaN (below every number), 2 an expert masked by a logit of
+// -inf under a selection bias (below every score, whatever the bias: the bias is not added),
+// else increasing with v. Without a bias the logit -inf is the lowest number by itself.
+constexpr uint32_t MASKED = 2u;
 __device__ __forceinline__ uint32_t key32(float v) {
     if (v != v) return 1u;
     const uint32_t u = __float_as_uint(v + 0.f);  // -0 and +0 tie
@@ -35,6 +38,11 @@ __device__ __forceinline__ uint64_t key64(double v) {
     if (v != v) return 1ull;
     const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
     return (u >> 63) ? ~u : u | (1ull << 63);
+}
+
+// sigmoid(l) + b in 64 bits, as a key.
+__device__ __forceinline__ uint64_t biased_key(float l, float b) {
+    return l == -INFINITY ? (uint64_t)MASKED : key64(1.0 / (1.0 + exp(-(double)l)) + (double)b);
 }
 
 struct GateParams {
@@ -55,8 +63,7 @@ __device__ __forceinline__ void choose(const GateParams &P, const float (&l)[V],
     for (int j = 0; j < V; j++) {
         const uint32_t e = j * 32u + lane;
         if constexpr (BIAS) {
-            const uint64_t key =
-                e < P.E ? key64(1.0 / (1.0 + exp(-(double)l[j])) + (double)__ldg(P.bias + e)) : 0ull;
+            const uint64_t key = e < P.E ? biased_key(l[j], __ldg(P.bias + e)) : 0ull;
             hi[j] = (uint32_t)(key >> 32);
             lo[j] = (uint32_t)key;
         } else {
@@ -114,7 +121,7 @@ __device__ __forceinline__ bool choose_few(const GateParams &P, const float (&l)
         const uint32_t e = j * 32u + lane;
         v[j] = e < P.E ? __fdividef(1.f, 1.f + __expf(-l[j])) + __ldg(P.bias + e) : 0.f;
         const float d = isinf(v[j]) ? 0.f : fmaf(fabsf(v[j]), 0x1p-23f, 0x1p-20f);
-        low[j] = e < P.E ? key32(v[j] - d) : 0u;
+        low[j] = e >= P.E ? 0u : l[j] == -INFINITY ? MASKED : key32(v[j] - d);
     }
     uint32_t cut = 0, n = 0;
     while (n < P.k) {  // takes away all that are as large as the largest left; k <= E
@@ -132,7 +139,7 @@ __device__ __forceinline__ bool choose_few(const GateParams &P, const float (&l)
     for (int j = 0; j < V; j++) {
         const uint32_t e = j * 32u + lane;
         const float d = isinf(v[j]) ? 0.f : fmaf(fabsf(v[j]), 0x1p-23f, 0x1p-20f);
-        const bool in = e < P.E && key32(v[j] + d) >= cut;
+        const bool in = e < P.E && (l[j] == -INFINITY ? MASKED : key32(v[j] + d)) >= cut;
         const uint32_t who = __ballot_sync(FULL, in), at = c + __popc(who & ((1u << lane) - 1u));
         if (in && at < 32u) few[at] = e;
         c += __popc(who);
@@ -144,7 +151,7 @@ __device__ __forceinline__ bool choose_few(const GateParams &P, const float (&l)
     if (lane < c) {
         mine = few[lane];
         const float x = load_x(P.logits, P.dtype, row + mine);
-        const uint64_t key = key64(1.0 / (1.0 + exp(-(double)x)) + (double)__ldg(P.bias + mine));
+        const uint64_t key = biased_key(x, __ldg(P.bias + mine));
         hi = (uint32_t)(key >> 32);
         lo = (uint32_t)key;
     }
