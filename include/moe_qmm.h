@@ -404,7 +404,9 @@ typedef struct {
  *     8-byte aligned (AUTO only): grouped products over tiles of 24 pairs, then
  *     moe_combine's kernel;
  *   otherwise moe_qmm_id_glu's and moe_qmm_id's paths (with MOE_PATH_AUTO, DECODE or
- *     GROUPED as given), then moe_combine's kernel.
+ *     GROUPED as given), then moe_combine's kernel. In the grouped GEMM affine and codebook
+ *     weights are two bf16 terms for bf16 and f32 x, of f32's range; two f16 terms for f16 x,
+ *     which end at 65,504 and are off by up to 2^-25.
  * h has 11 significant bits, under a power of two for each 32 values, in the first two
  * ways for a 16-bit result (22 in the few-token kernels for f16); 22 for an f32 result;
  * in the last way it is bf16 for bf16 x and f32 otherwise. The second way scales x by one

@@ -266,11 +266,15 @@ moe_status run(const void *x, const uint32_t *ids, const void *packed, const voi
         // bf16's per-token powers of two), when the workspace has room; not for MXFP4
         // (e2m1 * 2^e can leave f16's range), pointer tables, gated outputs or W4A4's
         // operand. With 64-pair tiles (a few pairs per expert) writing the image costs
-        // more than the GEMM saves.
+        // more than the GEMM saves. Inside moe_mlp gated outputs take it too, but bf16 x
+        // only with NVFP4 weights, which f16 holds exactly: affine and codebook weights
+        // would become f16 terms, infinite above 65,504 and off by up to 2^-25, where
+        // bf16 terms have f32's range.
+        const bool fits_f16 = a.kind == K_NVFP4 || x_dtype == MOE_F16;
         uint8_t *ximg = nullptr;
         float *tscale = nullptr;
         if (choice == GROUPED && !w4mma && tile_rows == 256u && x_dtype != MOE_F32 && a.kind != K_MXFP4 &&
-            !a.packed_ptrs && (a.act < 0 || layer) && !a.tok_scale && !a.x_copies && ((uintptr_t)x & 15u) == 0) {
+            !a.packed_ptrs && (layer ? fits_f16 : a.act < 0) && !a.tok_scale && !a.x_copies && ((uintptr_t)x & 15u) == 0) {
             const uint64_t ib = x_image_bytes(R, num_experts, k, tile_rows);
             if (workspace_bytes >= L.total + ib + al256(4ull * m)) {
                 ximg = ws + L.total;

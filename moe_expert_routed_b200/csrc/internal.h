@@ -134,10 +134,11 @@ cudaError_t launch_combine(const void *z, const float *weights, const uint32_t *
                            cudaStream_t st);
 
 // A product inside moe_mlp: what moe_qmm_id_glu / _bias / _path run, and what the layer's
-// two products share. With `layer` set, a gated output of 256-pair tiles takes the f16
-// image of x where the workspace has room, the routing left in the workspace by the
-// product before it (tiles of `routed` rows; 0: none) is taken over, and rows of pairs
-// with an id out of range are then not written.
+// two products share. With `layer` set, a gated output of 256-pair tiles may take the f16
+// image of x too, and either product takes it only where f16 holds the weights as well as
+// x's type does (NVFP4, or f16 x); the routing left in the workspace by the product before
+// it (tiles of `routed` rows; 0: none) is taken over, and rows of pairs with an id out of
+// range are then not written.
 struct LayerProduct {
     uint32_t routed;
 };
