@@ -409,7 +409,7 @@ typedef struct {
  *     which end at 65,504 and are off by up to 2^-25.
  * h has 11 significant bits, under a power of two for each 32 values, in the first two
  * ways for a 16-bit result (22 in the few-token kernels for f16); 22 for an f32 result;
- * in the last way it is bf16 for bf16 x and f32 otherwise. The second way scales x by one
+ * in the last way it is bf16 for bf16 x and a bf16 result, f32 otherwise. The second way scales x by one
  * power of two a token: values below 2^-39 of its largest count as 0. The products and
  * the sum are accumulated in f32 and out is rounded once. A value of x or h that is not
  * finite makes the results that it enters not finite. Errors as moe_qmm_id_glu and

@@ -16,11 +16,14 @@ namespace {
 
 inline size_t al256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// Type of h between the two products. bf16 x: bf16, the rounding every bf16 model
-// makes there (it adds 2^-9 of each h once, next to the 2^-9 of the result's own
-// rounding, and has f32's range). f16 and f32 x: f32, since |h| can leave f16's
-// range (two factors) and bf16 would cost an f16 result 3 of its bits.
-moe_dtype h_dtype(int x_dtype) { return x_dtype == DT_BF16 ? MOE_BF16 : MOE_F32; }
+// Type of h between the two products. bf16 x and a bf16 result: bf16, the rounding every
+// bf16 model makes there (it adds 2^-9 of each h once, next to the 2^-9 of the result's own
+// rounding, and has f32's range). Otherwise f32: |h| can leave f16's range (two factors),
+// and bf16 would cost an f16 result 3 of its bits and an f32 result 7 more of those that
+// the split of f32 operands into two bf16 terms leaves (16).
+moe_dtype h_dtype(int x_dtype, int out_dtype) {
+    return x_dtype == DT_BF16 && out_dtype == DT_BF16 ? MOE_BF16 : MOE_F32;
+}
 
 struct Layout {
     size_t own, h, z, total;  // own: workspace of the products, at offset 0 (the error word first)
@@ -29,14 +32,15 @@ struct Layout {
 bool layout(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t S, uint32_t E, int x_dtype, Layout *L) {
     const uint64_t R = (uint64_t)m * S;
     if (R > 0x7FFFFFFFull) return false;
-    const moe_dtype hd = h_dtype(x_dtype);
     const uint64_t few = mlp_few_workspace(m, hidden, inter, S);
     const size_t a = moe_qmm_id_workspace_bytes_k(m, hidden, S, E, (moe_dtype)x_dtype);
-    const size_t b = moe_qmm_id_workspace_bytes_k((uint32_t)R, inter, 1, E, hd);
-    if (!a || !b) return false;
-    L->own = al256(a > b ? a : b);
+    // whatever the result's type, with room for either type of h
+    const size_t b = moe_qmm_id_workspace_bytes_k((uint32_t)R, inter, 1, E, MOE_F32);
+    const size_t c = x_dtype == DT_BF16 ? moe_qmm_id_workspace_bytes_k((uint32_t)R, inter, 1, E, MOE_BF16) : b;
+    if (!a || !b || !c) return false;
+    L->own = al256(tmax(a, tmax(b, c)));
     L->h = L->own;
-    L->z = L->h + al256(R * inter * (hd == MOE_F32 ? 4ull : 2ull));
+    L->z = L->h + al256(R * inter * 4ull);
     L->total = L->z + al256(R * hidden * 4ull);
     // the few-token kernels' planes of h take the same room
     const uint64_t mid = mlp_mid_workspace(m, hidden, inter, S, E);
@@ -112,7 +116,7 @@ moe_status moe_mlp(const void *x, const uint32_t *ids, const float *weights, con
     if (path != MOE_PATH_GROUPED && (path == MOE_PATH_DECODE || R <= few_to) && mlp_few_supported(a))
         return launch_mlp_few(a, (uint32_t *)ws, h, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     if (mid) return launch_mlp_mid(a, ws, ws + L.h, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
-    const moe_dtype hd = h_dtype((int)x_dtype);
+    const moe_dtype hd = h_dtype((int)x_dtype, (int)out_dtype);
     LayerProduct layer{0u};
     v = run_product(x, ids, *gate_up, h, m, hidden, 2u * inter, n_expert_used, num_experts, x_dtype, hd, (int)act,
                     workspace, L.own, stream, path, &layer);

@@ -93,3 +93,16 @@ def test_weights_outside_the_range_of_f16(fmt, power, which):
     else:
         L.dn = scaled(L.dn, power)
     check(L, build(L, out_dtype=DT_BF16)(*inputs(L)), DT_BF16)
+
+
+@pytest.mark.parametrize("x_dtype", [DT_BF16, DT_F16])
+@pytest.mark.parametrize("fmt", ["aff4", "cb3", "nvfp4"])
+def test_f32_results_of_narrow_tokens(fmt, x_dtype):
+    """f32 results keep more than h in bf16 would (2^-9 each, 2^-9.8 of the norm): by the norm, the
+    roundings of two-term operands, 2^-16 each of gate (slopes of the activation up to 1.2), up,
+    h, down and the remainders' product, 5.2 * 2^-16, and the f32 sums and the activation, 2^-17
+    together: below 2^-13."""
+    L = layer_of(fmt, x_dtype, hidden=256, inter=160)
+    got = build(L, out_dtype=DT_F32)(*inputs(L)).cpu().double().numpy()
+    ref = L.reference(DT_F32)[0]
+    assert np.linalg.norm(got - ref) <= 2.0**-13 * np.linalg.norm(ref)
