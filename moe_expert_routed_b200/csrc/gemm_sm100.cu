@@ -1197,7 +1197,7 @@ cudaError_t launch_tp(const GemmParams &P0, const CUtensorMap &tmap, const CUten
     GemmParams P = P0;
     P.stages = (uint32_t)pl.stages;
     auto kern = grouped_gemm_kernel<KIND, XT, BN, PTRS, GLU, XIMG>;
-    static int smem_set[64];
+    static SmemSet smem_set;
     cudaError_t e = ensure_dyn_smem(kern, pl.smem, smem_set);
     if (e != cudaSuccess) return e;
     // persistent: one CTA per SM, or fewer when there are fewer work items

@@ -480,7 +480,7 @@ cudaError_t launch_gemm_w4a4(const QmmArgs &a, const uint8_t *xcodes, const uint
     if (S > W4_MAX_STAGES) S = W4_MAX_STAGES;
     P.stages = S;
     const size_t smem = (size_t)S * W4_STAGE + 1024;
-    static int smem_set[64];
+    static SmemSet smem_set;
     cudaError_t e = ensure_dyn_smem(gemm_w4a4_kernel, smem, smem_set);
     if (e != cudaSuccess) return e;
     const uint64_t items = (uint64_t)P.n_mtiles * max_tiles;

@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include "dyn_smem.h"
 #include "moe_qmm.h"
 #include <stddef.h>
 #include <stdint.h>
@@ -43,19 +44,6 @@ cudaError_t launch_route(const uint32_t *ids, uint32_t R, uint32_t E, uint32_t t
                          uint32_t *chunk_hist, uint32_t *chunk_base, uint32_t chunks,
                          uint32_t *err, void *out, uint32_t n, int out_dtype, cudaStream_t st,
                          uint32_t *work_counter = nullptr);
-
-// cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per kernel and device:
-// `cache` is a per-kernel array of the largest size already set, per device.
-template <typename K>
-inline cudaError_t ensure_dyn_smem(K kern, size_t bytes, int (&cache)[64]) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64 && cache[dev] >= (int)bytes) return cudaSuccess;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess && dev >= 0 && dev < 64) cache[dev] = (int)bytes;
-    return e;
-}
 
 struct QmmArgs {
     const void *x;

@@ -803,7 +803,7 @@ template <int MODE, int PLANES, int NB>
 cudaError_t up_t(const FewParams &P, cudaStream_t st) {
     const size_t smem = up_bytes(MODE, P.H, P.g1, PLANES, NB);
     auto kern = mlp_up<MODE, PLANES, NB>;
-    static int smem_set[64];
+    static SmemSet smem_set;
     const cudaError_t e = ensure_dyn_smem(kern, smem, smem_set);
     if (e != cudaSuccess) return e;
     // about two waves of two CTAs an SM if every pair has an expert of its own: further
@@ -818,7 +818,7 @@ template <int MODE, int NPL, int NB, int T>
 cudaError_t down_t(FewParams P, cudaStream_t st) {
     const size_t smem = down_bytes(MODE, P.I, P.g2, NPL, NB, T, P.m);
     auto kern = mlp_down<MODE, NPL, NB, T>;
-    static int smem_set[64];
+    static SmemSet smem_set;
     const cudaError_t e = ensure_dyn_smem(kern, smem, smem_set);
     if (e != cudaSuccess) return e;
     const uint32_t steps = (P.I / 32u + 3u) / 4u;

@@ -541,7 +541,7 @@ template <int MODE, bool UP>
 cudaError_t product(const MidParams &P, uint32_t max_tiles, cudaStream_t st) {
     auto kern = mid_product<MODE, UP>;
     const size_t smem = (size_t)ring(MODE) * stage_bytes(MODE);
-    static int smem_set[64];
+    static SmemSet smem_set;
     const cudaError_t e = ensure_dyn_smem(kern, smem, smem_set);
     if (e != cudaSuccess) return e;
     // a programmatic dependent of the kernel before it, which saves the launch's latency
