@@ -511,7 +511,7 @@ template <int NPB, bool FUSED>
 cudaError_t launch_dp4a_one(const GemvParams &P, dim3 grid, cudaStream_t st) {
     const size_t smem = dp4a_smem(P, NPB);
     auto kern = gemv_aff4_dp4a<NPB, FUSED>;
-    if (smem > 48 * 1024) {
+    if (smem > SMEM_FREE) {
         static SmemSet smem_set;
         cudaError_t e = ensure_dyn_smem(kern, smem, smem_set);
         if (e != cudaSuccess) return e;
@@ -1188,7 +1188,7 @@ void rows_shape(uint32_t nu, int *lpr, int *upl) {
 template <int LPR, int UPL, bool GLU>
 cudaError_t launch_rows_t(const GemvParams &P, uint32_t rb, uint32_t ctas, size_t smem, cudaStream_t st) {
     auto kern = gemv_aff4_rows<LPR, UPL, GLU>;
-    if (smem > 48 * 1024) {
+    if (smem > SMEM_FREE) {
         static SmemSet smem_set;
         cudaError_t e = ensure_dyn_smem(kern, smem, smem_set);
         if (e != cudaSuccess) return e;
@@ -1311,7 +1311,7 @@ cudaError_t launch_tma_one(const GemvParams &P, uint32_t ycount, cudaStream_t st
     const TmaLayout L = tma_layout(RB, P.row_bytes, spec ? P.m * P.k * xsz : NPB * P.k * xsz, NPB,
                                    P.n_units, P.groups);
     auto kern = gemv_aff4_tma<NPB, MODE, LPR>;
-    if (L.total > 48 * 1024) {
+    if (L.total > SMEM_FREE) {
         static SmemSet smem_set;
         cudaError_t e = ensure_dyn_smem(kern, L.total, smem_set);
         if (e != cudaSuccess) return e;
@@ -1356,7 +1356,7 @@ template <int KIND, int NPB, bool FUSED>
 cudaError_t launch_one(const GemvParams &P, dim3 grid, cudaStream_t st) {
     const size_t smem = (size_t)NPB * P.xstride * sizeof(float);
     auto kern = gemv_kernel<KIND, NPB, FUSED>;
-    if (smem > 48 * 1024) {
+    if (smem > SMEM_FREE) {
         static SmemSet smem_set;
         cudaError_t e = ensure_dyn_smem(kern, smem, smem_set);
         if (e != cudaSuccess) return e;

@@ -13,6 +13,9 @@ constexpr int GEMV_LPR = 8;                         // lanes per row
 constexpr int GEMV_ROWS = GEMV_THREADS / GEMV_LPR;  // 32 rows per CTA
 constexpr uint32_t FUSED_MAX_R = 64;
 constexpr size_t GEMV_SMEM_BUDGET = 200 * 1024;
+// Dynamic shared memory that a launch has without raising the kernel's limit: 48 KB
+// less the kernels' static arrays (under 2 KB), which count towards it.
+constexpr size_t SMEM_FREE = 44 * 1024;
 
 struct GemvParams {
     const void *x;
