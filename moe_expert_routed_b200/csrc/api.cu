@@ -202,6 +202,7 @@ moe_status run(const void *x, const uint32_t *ids, const void *packed, const voi
     a.fault_wait_ns = g_fault_wait_ns.load(std::memory_order_relaxed);
     a.x_copies = g_x_copies.load(std::memory_order_relaxed);
     a.tok_scale = nullptr;
+    a.full_x = layer != nullptr;
 
     uint8_t *ws = (uint8_t *)workspace;
     uint32_t *err = (uint32_t *)(ws + L.err);

@@ -1260,6 +1260,7 @@ uint32_t rows_per_cta(uint32_t total_rows, uint32_t G) {
 // at most 96 units (k <= 3072) per row, and the CTA's shared memory within budget.
 bool rows_ok(const QmmArgs &a) {
     if (a.m != 1 || a.n_expert_used > ROWS_MAX_PAIRS || !dp4a_ok(a)) return false;
+    if (a.full_x && a.x_dtype == DT_F32) return false;
     const uint32_t xsz = a.x_dtype == DT_F32 ? 4u : 2u;
     if ((a.k * xsz) % 16u != 0 || (uintptr_t)a.x % 16u != 0) return false;
     int lpr, upl;

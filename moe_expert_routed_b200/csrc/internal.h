@@ -69,6 +69,9 @@ struct QmmArgs {
     // W4A4 on the grouped GEMM: the GEMM takes x as these bf16 values and multiplies
     // each output by tok_scale[token] (null: x as given, no factor)
     const float *tok_scale;
+    // f32 x keeps its bits: not the one-token kernel, whose fixed point has 16 for a unit
+    // of 32 values (enough for 16-bit x, and for moe_qmm_id's tolerance)
+    bool full_x;
 };
 
 // CUDA-core GEMV with routing fused in (R <= 64).
@@ -126,7 +129,7 @@ cudaError_t launch_combine(const void *z, const float *weights, const uint32_t *
 // image of x too, and either product takes it only where f16 holds the weights as well as
 // x's type does (NVFP4, or f16 x); the routing left in the workspace by the product before
 // it (tiles of `routed` rows; 0: none) is taken over, and rows of pairs with an id out of
-// range are then not written.
+// range are then not written. f32 x and h keep their bits (full_x).
 struct LayerProduct {
     uint32_t routed;
 };
