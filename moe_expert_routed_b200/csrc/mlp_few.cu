@@ -470,19 +470,23 @@ __global__ void __launch_bounds__(FEW_THREADS, NB <= 2 ? 2 : 1) mlp_up(const Few
                 const int planes = h_planes(P.out_dtype);
                 const uint32_t un = unit & 3u;
                 uint8_t *img = P.hf + ((size_t)p_e * ((units + 3u) / 4u) + (unit >> 2)) * step_bytes(planes);
-                float sum = h;
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(FULL, sum, d);
                 float scale, factor;
                 unit_scale(__reduce_max_sync(FULL, __float_as_uint(h) & 0x7FFFFFFFu), scale, factor);
-                h *= scale;
-                if (P.down_order == 1 && planes == 1 && (lane & 1u)) h *= 0.0625f;  // meets a 16-fold pair
+                const bool part = P.down_order == 1 && planes == 1 && (lane & 1u);  // a sixteenth, meets a 16-fold pair
+                h *= part ? scale * 0.0625f : scale;
                 uint16_t *dst = (uint16_t *)(img + un * 64u) + b_place(P.down_order, lane);
-                for (int k = 0; k < planes; k++, dst += 128) {
+                // The sum that meets the affine biases is that of the rounded values, which the
+                // codes meet: a rounding then counts with the weight c s + b, not with c s, which
+                // is many times that in a group whose codes lie close together.
+                float sum = 0.f, plane = part ? factor * 16.f : factor;
+                for (int k = 0; k < planes; k++, dst += 128, plane *= 4.8828125e-4f) {  // 2^-11
                     const __half b = __float2half_rn(h);
                     *dst = __half_as_ushort(b);
+                    sum = fmaf(__half2float(b), plane, sum);
                     h = (h - __half2float(b)) * 2048.f;
                 }
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(FULL, sum, d);
                 float2 *fs = (float2 *)(img + planes * 256);
                 if (lane == 0) fs[un] = make_float2(factor, sum);
                 // units past inter in the last step are zero

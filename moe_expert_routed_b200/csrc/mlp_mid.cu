@@ -72,6 +72,7 @@ struct MidParams {
     uint32_t k, n, S;            // n: rows of out (UP: of gate, the up rows follow)
     uint32_t row_bytes, groups, gshift;
     int bias_dtype, act, order;  // order of h's values in its images
+    int sums;                    // UP: the down projection is affine and needs sums of h
 };
 
 // Two f32 values in one 64-bit register pair.
@@ -414,18 +415,23 @@ __global__ void __launch_bounds__(MID_THREADS, ctas(MODE)) mid_product(const Mid
         const uint32_t end = blockIdx.x + 1u == gridDim.x ? 4u * hsteps : u0 + HU;
         for (uint32_t o = warp; o < (end - u0) * np; o += MID_WARPS) {
             const uint32_t pr = o / (end - u0), un = u0 + o % (end - u0);
-            float h = un < units ? hb[pr * HB + (un - u0) * 32u + lane] : 0.f, sum = h;  // zeros past the last column
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(FULL, sum, d);
+            const float h = un < units ? hb[pr * HB + (un - u0) * 32u + lane] : 0.f;  // zeros past the last column
             float scale, factor;
             unit_scale(__reduce_max_sync(FULL, __float_as_uint(h) & 0x7FFFFFFFu), scale, factor);
-            h *= scale;
-            if (P.order == 1 && (lane & 1u)) h *= 0.0625f;  // meets a 16-fold pair
+            const bool part = P.order == 1 && (lane & 1u);  // a sixteenth, meets a 16-fold pair
+            const __half b = __float2half_rn(part ? h * scale * 0.0625f : h * scale);
+            // The sum that meets the affine biases is that of the rounded values, which the codes
+            // meet: a rounding then counts with the weight c s + b, not with c s, which is many
+            // times that in a group whose codes lie close together.
+            float sum = __half2float(b) * (part ? 16.f / CODE_UNIT : 1.f / CODE_UNIT);
+            if (P.sums)
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(FULL, sum, d);
             uint8_t *img = (uint8_t *)P.out + ((size_t)(place + pr) * hsteps + (un >> 2)) * step_bytes(1);
-            ((uint16_t *)(img + (un & 3u) * 64u))[b_place(P.order, lane)] = __half_as_ushort(__float2half_rn(h));
+            ((uint16_t *)(img + (un & 3u) * 64u))[b_place(P.order, lane)] = __half_as_ushort(b);
             if (lane == 0) {
                 ((float *)(img + 256u))[un & 3u] = factor;
-                ((float *)(img + 272u))[un & 3u] = sum * (1.f / CODE_UNIT);
+                ((float *)(img + 272u))[un & 3u] = sum * factor;
             }
         }
     }
@@ -629,7 +635,7 @@ cudaError_t launch_mlp_mid(const MlpArgs &a, uint8_t *ws, uint8_t *own, cudaStre
     P.k = a.hidden; P.n = a.inter; P.S = a.S;
     P.row_bytes = (uint32_t)moe_packed_row_bytes(a.gate_up->fmt, a.gate_up->bits, a.hidden);
     P.groups = a.hidden / a.gate_up->group_size; P.gshift = log2_units(*a.gate_up);
-    P.act = a.act; P.order = order_of(m2);
+    P.act = a.act; P.order = order_of(m2); P.sums = affine(m2);
     e = product_m<true>(P, m1, max_tiles, st);
     if (e != cudaSuccess) return e;
     P.w = (const uint8_t *)a.down->packed; P.s = (const uint8_t *)a.down->scales;
