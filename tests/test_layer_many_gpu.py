@@ -106,3 +106,39 @@ def test_f32_results_of_narrow_tokens(fmt, x_dtype):
     got = build(L, out_dtype=DT_F32)(*inputs(L)).cpu().double().numpy()
     ref = L.reference(DT_F32)[0]
     assert np.linalg.norm(got - ref) <= 2.0**-13 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("m,top_k,E_", [(5, 2, 8), (60, 3, 6), (300, 2, 4)])  # the three ways
+@pytest.mark.parametrize("fmt", ["aff4", "nvfp4"])
+def test_no_pair_left(fmt, m, top_k, E_):
+    """Every id out of range: the residual alone, or zeros."""
+    f, bits, gs = FORMATS[fmt]
+    L = LR.Layer(m=m, hidden=128, inter=64, top_k=top_k, E=E_, fmt=f, bits=bits, gs=gs, x_dtype=DT_BF16, seed=m)
+    layer = build(L, out_dtype=DT_BF16)
+    x, ids, w = inputs(L)
+    res = torch.from_numpy(L.res).to(torch.bfloat16).cuda()
+    none = torch.full_like(ids, E_)
+    assert torch.equal(layer(x, none, w, residual=res), res)
+    assert torch.count_nonzero(layer(x, none, w)) == 0 and M.poll_error(layer.workspace) == 5
+    check(L, layer(x, ids, w), DT_BF16)
+    assert M.poll_error(layer.workspace) == 0
+
+
+@pytest.mark.parametrize("fmt,x_dtype", [("nvfp4", DT_BF16), ("cb3", DT_F16), ("aff4", DT_BF16)])
+def test_many_pairs_captured_and_replayed_with_other_inputs(fmt, x_dtype):
+    Ls = [layer_of(fmt, x_dtype, hidden=96, inter=64, seed=s) for s in (3, 3)]
+    rng = np.random.default_rng(1)
+    Ls[1].gu = Ls[1].gu.with_ids(rng.integers(0, E, (M_TOKENS, 2)).astype(np.uint32)).with_x(Ls[0].gu.x[::-1].copy())
+    layer = build(Ls[0], out_dtype=x_dtype)
+    x, ids, w = (t.clone() for t in inputs(Ls[0]))
+    layer(x, ids, w)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer(x, ids, w)
+    for L in (Ls[1], Ls[0]):
+        for to, t in zip((x, ids, w), inputs(L)):
+            to.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(L, out, x_dtype)
