@@ -258,8 +258,10 @@ size_t moe_qmm_id_workspace_bytes(uint32_t m, uint32_t n_expert_used, uint32_t n
  *              room is added for smaller calls): bf16 x is scaled by a
  *              power of two per token (exact in f16 above 2^-28 of the token's largest
  *              value) and the factor is undone in the epilogue. Each k-tile of a tile
- *              is then one bulk copy. Not for MXFP4 weights, pointer tables or gated
- *              outputs, which keep the row copies.
+ *              is then one bulk copy. Affine and codebook weights are then two f16 terms
+ *              for bf16 x as for f16 x: they end at 65,504 and are off by up to 2^-25
+ *              (without the image two bf16 terms, of f32's range). Not for MXFP4
+ *              weights, pointer tables or gated outputs, which keep the row copies.
  * With the minimum moe_qmm_id_workspace_bytes the GEMM's loader warps copy x rows
  * themselves. k must be a multiple of 8 (else no room is added). Returns 0 if the
  * sizes overflow or x_dtype is not a moe_dtype. */
@@ -409,10 +411,16 @@ typedef struct {
  *     which end at 65,504 and are off by up to 2^-25.
  * h has 11 significant bits, under a power of two for each 32 values, in the first two
  * ways for a 16-bit result (22 in the few-token kernels for f16); 22 for an f32 result;
- * in the last way it is bf16 for bf16 x and a bf16 result, f32 otherwise. The second way scales x by one
- * power of two a token: values below 2^-39 of its largest count as 0. The products and
- * the sum are accumulated in f32 and out is rounded once. A value of x or h that is not
- * finite makes the results that it enters not finite. Errors as moe_qmm_id_glu and
+ * in the last way it is bf16 for bf16 x and a bf16 result, f32 otherwise. (With 4-bit affine
+ * codes half of the values of 32 keep the 11 bits down to 2^-24 of the largest, the others
+ * and other codes down to 2^-28.) 16-bit x is held in f16 under a power of two, one for each
+ * 32 values in the first way, for each token in the second and, with NVFP4 weights, in the
+ * grouped GEMM: exact down to 2^-31 (bf16) or 2^-28 (f16) of the largest value there and off
+ * by at most 2^-39 of it below; in the first two ways 2^-27, 2^-24 and 2^-35 with 4-bit
+ * affine codes. In those two, values of x and h above 2^115 can give infinities (codebook
+ * entries up to 8): 32 products with the bare codes are summed before their scale. The
+ * products and the sum are accumulated in f32 and out is rounded once. A value of x or h that
+ * is not finite makes the results that it enters not finite. Errors as moe_qmm_id_glu and
  * moe_combine.
  */
 #define MOE_MLP_FEW_TOKENS 64u

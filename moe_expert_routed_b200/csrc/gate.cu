@@ -12,7 +12,7 @@
 // on the logits themselves and is exact. With a bias the choice is by sigmoid(l) + b:
 // two experts can then lie closer than a 32-bit sigmoid tells apart, so that sum is
 // formed in 64 bits and compared as a 64-bit key (two redux rounds). The 64-bit
-// exponentials would bound it (8,192 x 256: 23 us against 17), so they are taken only of the
+// exponentials would bound it (8,192 x 256: 23 us against 17; 257 x 160: 6.5), so they are taken only of the
 // experts that a 32-bit score with its error bound cannot rule out: as a rule the k
 // chosen and few more, one a lane.
 #include "common.cuh"
@@ -107,9 +107,9 @@ __device__ __forceinline__ void choose(const GateParams &P, const float (&l)[V],
 
 // The same with a selection bias, among the experts whose 32-bit score may reach the k-th:
 // false if there are more than 32 of those. The score is off by less than 2^-21: of the
-// sigmoid s, s (1 - s) (2 + 1.16 |l|) 2^-23 < 2^-24 by __expf, 2^-24 by the sum, 2^-22 by
-// __fdividef (2 units in the last place); and 2^-24 of the sum with the bias. Twice
-// that is allowed for. An expert among the k best scores no less than the k-th largest lower
+// sigmoid s, s (1 - s) (2 + 1.16 |l|) 2^-23 < 1.3 * 2^-24 by __expf (its largest value is near
+// |l| = 0.8), 2^-24 by the sum, 2^-22 by __fdividef (2 units in the last place); and 2^-24
+// of the sum with the bias. Twice that is allowed for. An expert among the k best scores no less than the k-th largest lower
 // bound, so its upper bound does not lie below that.
 template <int V>
 __device__ __forceinline__ bool choose_few(const GateParams &P, const float (&l)[V], size_t row, uint32_t *few,

@@ -105,7 +105,8 @@ moe_status moe_mlp(const void *x, const uint32_t *ids, const float *weights, con
     // 204 / 192 (3-bit codebook), 221 / 157 (affine 8 bits); at 1 pair 184 / 199, 193 / 172, 376 /
     // 292, 391 / 232; at 2 pairs 288 / 261, 313 / 227, 531 / 390, 604 / 306. Of 8 experts, 16 pairs
     // in all 23 / 33, 23 / 29, 38 / 40, 40 / 39; 32 pairs 40 / 34, 42 / 32, 48 / 40, 53 / 40.
-    // Where mlp_mid.cu does not apply (32-bit types) the grouped products are left: few
+    // (The codebooks of 2 and 4 bits and 6-bit codes follow the 3-bit codebook, MXFP4 follows
+    // NVFP4, by likeness.) Where mlp_mid.cu does not apply (32-bit types) the grouped products are left: few
     // against grouped, 16-bit types, at 4 pairs an expert 110 / 177 (affine 4 bits), 116 / 128
     // (NVFP4), 147 / 180 (affine 8 bits), at 8 171 / 179, 179 / 131, 268 / 183; 64 pairs of 8
     // experts 49 / 79, 52 / 63, 66 / 83.

@@ -20,8 +20,8 @@
 // converted to f16 before the legacy MMA anyway and took twice the instructions.
 //   x and h enter as f16 planes: a unit of 32 values is scaled by a power of two to below
 // 2^15, the first plane is its rounding to f16, the second that of the remainder. One
-// plane holds bf16 and f16 x exactly (down to 2^-38 of the unit's largest value); f32 x
-// takes two, 22 bits. h, the f32 result of mlp_up, takes one for a bf16 result (11
+// plane holds bf16 x exactly down to 2^-31 of the unit's largest value and f16 x down to
+// 2^-28 (2^-27 and 2^-24 where x meets 16-fold codes); f32 x takes two, 22 bits. h, the f32 result of mlp_up, takes one for a bf16 result (11
 // bits, 3 more than the rounding to bf16 that the result gets anyway) and two otherwise.
 //   Scales of weights and of x are applied to f32 sums of one unit. The four lanes
 // that share a row each hold another unit (their 16-byte load), so a column belongs to

@@ -13,9 +13,10 @@
 // take a quarter of the same unit each (of the same scale's 16 codes, NVFP4).
 //
 // x is scaled by one power of two a token, h by one a unit; both are one f16 plane: exact
-// for 16-bit x (down to 2^-39 of the token's largest value), 11 bits of h, whose rounding
-// adds less to a 16-bit result than its own does (f16: 2.9e-4 against 64 bits instead of
-// 2.1e-4; bf16: nothing to be seen). f32 types take the other ways.
+// for bf16 x down to 2^-31 of the token's largest value and for f16 x down to 2^-28 (2^-27
+// and 2^-24 where x meets 16-fold codes), off by at most 2^-39 (2^-35) of it below; 11 bits
+// of h, whose rounding adds no more to a 16-bit result than its own does (f16: 2.9e-4
+// against 64 bits instead of 2.1e-4; bf16: nothing to be seen). f32 types take the other ways.
 //
 // A CTA: 128 weight rows, 32 a warp as two tiles, which share the registers of x; three to
 // five CTAs an SM. Steps of 128 codes come by cp.async into a ring of two or three stages,
@@ -24,8 +25,10 @@
 // CTAs: 242 us against 260 with tiles of 32 and four (affine 4 bits), 221 against 232.
 // Bound by instructions: for each unit and 32 rows 40 (affine 4 bits) to 90 (3-bit codebook)
 // to expand and scale the codes, 20 for each block of 8 pairs, 30 for copies and scales; the
-// scheduler issues in 57 % of its cycles, the ALU is busy for 46 %, MMA for 21 %.
-// 128 experts of 2,816 x 704, top-8, 256 tokens: 282 us (3-bit codebook; the tcgen05 grouped
+// scheduler issues in 54 to 57 % of its cycles, the ALU is busy for 49 %, MMA for 20 %. With no
+// products at all 142 of (then) 322 us are left: each CTA's chain of dependent loads and its
+// empty ring.
+// 128 experts of 2,816 x 704, top-8, 256 tokens: 281 us (3-bit codebook; the tcgen05 grouped
 // products 558), 224 (affine 4 bits; 554), 202 (NVFP4; 389), 247 (affine 8 bits; 561).
 #include "cb3_blocks.h"
 #include "common.cuh"
@@ -220,7 +223,7 @@ __device__ __forceinline__ void mid_step(uint32_t row, uint32_t xs, uint32_t fs,
     }
 }
 
-// grid (blocks of 256 rows, tiles).
+// grid (blocks of 128 rows, tiles).
 template <int MODE, bool UP>
 __global__ void __launch_bounds__(MID_THREADS, ctas(MODE)) mid_product(const MidParams P) {
     constexpr uint32_t LINE = line(MODE), XL = x_line(MODE), STAGE = stage_bytes(MODE), RINGS = ring(MODE);
@@ -588,7 +591,8 @@ uint32_t tiles_of(uint64_t R, uint32_t E) { return (uint32_t)(R / MID_PAIRS) + E
 // Up to MOE_MLP_MID_PAIRS pairs an expert, 24 with 6-bit codes. Measured against the grouped
 // products with 128 experts of 2,816 x 704, us: 24 pairs an expert 329 / 559 (affine 4 bits),
 // 299 / 395 (NVFP4), 419 / 579 (3-bit codebook), 477 / 566 (6 bits); 32 pairs 414 / 568, 378 / 404,
-// 534 / 590, 605 / 577.
+// 534 / 590, 605 / 577. The other formats were not measured beyond 16 pairs an expert (MXFP4 there
+// 236 / 829 us, so its crossing lies higher) and take the same limit.
 static uint64_t mid_limit(uint32_t E) { return tmin<uint64_t>((uint64_t)MOE_MLP_MID_PAIRS * E, 1u << 20); }
 
 uint64_t mlp_mid_workspace(uint32_t m, uint32_t hidden, uint32_t inter, uint32_t S, uint32_t E) {
