@@ -520,9 +520,12 @@ cudaError_t launch_dp4a_one(const GemvParams &P, dim3 grid, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+// Pairs a pass that the kernels are built for, which their shared memory goes by: 1, 2, 4, 8.
+uint32_t pair_slots(uint32_t npb) { return npb <= 2u ? npb : npb <= 4u ? 4u : 8u; }
+
 template <bool FUSED>
 cudaError_t launch_dp4a(const GemvParams &P, uint32_t npb, dim3 grid, cudaStream_t st) {
-    while (npb > 1 && dp4a_smem(P, (int)npb) > GEMV_SMEM_BUDGET) npb >>= 1;
+    while (npb > 1 && dp4a_smem(P, (int)pair_slots(npb)) > GEMV_SMEM_BUDGET) npb >>= 1;
     if (npb <= 1) return launch_dp4a_one<1, FUSED>(P, grid, st);
     if (npb <= 2) return launch_dp4a_one<2, FUSED>(P, grid, st);
     if (npb <= 4) return launch_dp4a_one<4, FUSED>(P, grid, st);
@@ -1370,7 +1373,7 @@ template <int KIND, bool FUSED>
 cudaError_t launch_npb(const GemvParams &P, uint32_t npb, dim3 grid, cudaStream_t st) {
     // keep the staged x rows within the shared-memory budget
     const size_t row_bytes = (size_t)P.xstride * sizeof(float);
-    while (npb > 1 && npb * row_bytes > GEMV_SMEM_BUDGET) npb >>= 1;
+    while (npb > 1 && pair_slots(npb) * row_bytes > GEMV_SMEM_BUDGET) npb >>= 1;
     if (row_bytes > GEMV_SMEM_BUDGET) return cudaErrorInvalidConfiguration;
     if (npb <= 1) return launch_one<KIND, 1, FUSED>(P, grid, st);
     if (npb <= 2) return launch_one<KIND, 2, FUSED>(P, grid, st);

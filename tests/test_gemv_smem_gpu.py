@@ -26,3 +26,18 @@ def test_staged_x_near_48_kb(fmt, bits, gs, k, m, E):
     assert M.poll_error(ws) == 0
     nviol, ratio, _ = check_full(P, out)
     assert nviol == 0, f"worst err / bound {ratio:.3g}"
+
+
+@pytest.mark.parametrize("fmt,bits,gs,k", [(FMT_CODEBOOK, 4, 64, 7936), (FMT_AFFINE, 4, 16, 7936),
+                                           (FMT_AFFINE, 4, 64, 7936), (FMT_NVFP4, 4, 16, 8192)])
+@pytest.mark.parametrize("m", [3, 5, 6, 7, 8])
+def test_long_rows_for_five_to_seven_tokens(fmt, bits, gs, k, m):
+    """Rows of which fewer than eight fit in shared memory: kernels have room for 1, 2, 4 or 8 pairs,
+    so five to seven count as eight."""
+    P = make_problem("long", fmt=fmt, bits=bits, group_size=gs, m=m, k=k, n=40, n_expert_used=1, num_experts=1,
+                     x_dtype=DT_F32, out_dtype=DT_F32, seed=m)
+    ws = M.new_workspace(P.m, 1, 1)
+    out = run(P, "decode", workspace=ws)
+    assert M.poll_error(ws) == 0
+    nviol, ratio, _ = check_full(P, out)
+    assert nviol == 0, f"worst err / bound {ratio:.3g}"
