@@ -21,7 +21,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["api.cu", "route.cu", "gemv.cu", "gemm_sm100.cu", "noalloc.cu", "actq.cu", "gemm_w4a4.cu",
            "gate.cu", "combine.cu", "mlp.cu", "mlp_few.cu", "mlp_mid.cu"]
 HEADERS = ["common.cuh", "ptx.cuh", "internal.h", "gemv_common.cuh", "mlp_codes.cuh", "cb3_blocks.h",
-           "dyn_smem.h"]
+           "dyn_smem.h", "status.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -242,13 +242,14 @@ moe_status run(const void *x, const uint32_t *ids, const void *packed, const voi
         a.tok_scale = w4->g;
         if (!gemm_supported(a)) return MOE_ERR_UNSUPPORTED;
     }
-    if (w4 && moe::launch_quant_act(w4->x, w4->x_dtype, m, k, w4mma ? w4->codes : nullptr,
-                                    w4mma ? w4->xs : nullptr, (w4mma || w4x16) ? w4->g : nullptr,
-                                    (w4mma || w4x16) ? nullptr : w4->xhat, w4x16 ? w4->x16 : nullptr,
-                                    (cudaStream_t)stream) != cudaSuccess)
-        return MOE_ERR_CUDA;
-
     cudaError_t ce;
+    if (w4) {
+        ce = moe::launch_quant_act(w4->x, w4->x_dtype, m, k, w4mma ? w4->codes : nullptr, w4mma ? w4->xs : nullptr,
+                                   (w4mma || w4x16) ? w4->g : nullptr, (w4mma || w4x16) ? nullptr : w4->xhat,
+                                   w4x16 ? w4->x16 : nullptr, (cudaStream_t)stream);
+        if (ce != cudaSuccess) return status_of(ce);
+    }
+
     if (choice == FUSED) {
         ce = launch_gemv_fused(a, err, st);
     } else {
@@ -307,7 +308,7 @@ moe_status run(const void *x, const uint32_t *ids, const void *packed, const voi
                 ce = launch_gemv_routed(a, counts, offsets, sp, err, st);
         }
     }
-    return ce == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return status_of(ce);
 }
 
 }  // namespace
@@ -384,11 +385,8 @@ moe_status moe_quantize_act_nvfp4(const void *x, uint32_t m, uint32_t k, moe_dty
     if (((uintptr_t)codes & 3u) || ((uintptr_t)xhat & 15u) || ((uintptr_t)gscale & 3u))
         return MOE_ERR_INVALID_ARGUMENT;
     if (k % 16u != 0) return MOE_ERR_UNSUPPORTED;
-    return moe::launch_quant_act(x, (int)x_dtype, m, k, codes, scales, gscale, xhat, nullptr,
-                                 (cudaStream_t)stream) ==
-                   cudaSuccess
-               ? MOE_OK
-               : MOE_ERR_CUDA;
+    return status_of(moe::launch_quant_act(x, (int)x_dtype, m, k, codes, scales, gscale, xhat, nullptr,
+                                           (cudaStream_t)stream));
 }
 
 moe_status moe_qmm_id_w4a4(const void *x, const uint32_t *ids, const void *packed, const void *scales,
@@ -529,7 +527,7 @@ moe_status moe_qmm_id_route(const uint32_t *ids, uint32_t m, uint32_t n_expert_u
                                   (uint32_t *)(ws + L.chunk_hist), (uint32_t *)(ws + L.chunk_base),
                                   L.chunks, (uint32_t *)(ws + L.err), nullptr, 0, 0,
                                   (cudaStream_t)stream);
-    return ce == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return status_of(ce);
 }
 
 moe_status moe_qmm_test_inject_wait_timeout(uint64_t limit_ns) {
@@ -547,13 +545,13 @@ moe_status moe_qmm_id_poll_error(void *workspace, moe_stream_t stream) {
     if (!workspace) return MOE_ERR_INVALID_ARGUMENT;
     cudaStream_t st = (cudaStream_t)stream;
     uint32_t w = 0;
-    if (cudaMemcpyAsync(&w, workspace, sizeof(w), cudaMemcpyDeviceToHost, st) != cudaSuccess)
-        return MOE_ERR_CUDA;
-    if (cudaStreamSynchronize(st) != cudaSuccess) return MOE_ERR_CUDA;
-    if (w) {
-        if (cudaMemsetAsync(workspace, 0, sizeof(w), st) != cudaSuccess) return MOE_ERR_CUDA;
-        if (cudaStreamSynchronize(st) != cudaSuccess) return MOE_ERR_CUDA;
+    cudaError_t ce = cudaMemcpyAsync(&w, workspace, sizeof(w), cudaMemcpyDeviceToHost, st);
+    if (ce == cudaSuccess) ce = cudaStreamSynchronize(st);
+    if (ce == cudaSuccess && w) {
+        ce = cudaMemsetAsync(workspace, 0, sizeof(w), st);
+        if (ce == cudaSuccess) ce = cudaStreamSynchronize(st);
     }
+    if (ce != cudaSuccess) return status_of(ce);
     if (w & ERR_TIMEOUT) return MOE_ERR_TIMEOUT;
     if (w & ERR_BAD_ID) return MOE_ERR_BAD_EXPERT_ID;
     if (w & ERR_BAD_POINTER) return MOE_ERR_BAD_EXPERT_POINTER;

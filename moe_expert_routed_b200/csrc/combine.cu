@@ -165,8 +165,6 @@ extern "C" moe_status moe_combine(const void *z, const float *weights, const uin
         (((uintptr_t)weights | (uintptr_t)ids) & 3u))
         return MOE_ERR_INVALID_ARGUMENT;
     if ((uint64_t)m * n_expert_used > 0x7FFFFFFFull) return MOE_ERR_UNSUPPORTED;
-    return moe::launch_combine(z, weights, ids, residual, out, m, n_expert_used, n, num_experts, (int)z_dtype,
-                               (int)out_dtype, (cudaStream_t)stream) == cudaSuccess
-               ? MOE_OK
-               : MOE_ERR_CUDA;
+    return moe::status_of(moe::launch_combine(z, weights, ids, residual, out, m, n_expert_used, n, num_experts,
+                                              (int)z_dtype, (int)out_dtype, (cudaStream_t)stream));
 }

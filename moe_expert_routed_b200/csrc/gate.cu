@@ -264,7 +264,6 @@ extern "C" moe_status moe_gate_topk(const void *logits, const float *select_bias
         return MOE_ERR_UNSUPPORTED;
     const moe::GateParams P{logits, select_bias, ids, weights, m, num_experts, top_k, (int)logits_dtype,
                             score == MOE_SCORE_SIGMOID, renormalize != 0, scale};
-    const cudaError_t ce =
-        select_bias ? moe::launch_v<true>(P, (cudaStream_t)stream) : moe::launch_v<false>(P, (cudaStream_t)stream);
-    return ce == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return moe::status_of(select_bias ? moe::launch_v<true>(P, (cudaStream_t)stream)
+                                      : moe::launch_v<false>(P, (cudaStream_t)stream));
 }

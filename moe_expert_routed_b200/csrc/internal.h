@@ -5,6 +5,7 @@
 
 #include "dyn_smem.h"
 #include "moe_qmm.h"
+#include "status.h"
 #include <stddef.h>
 #include <stdint.h>
 

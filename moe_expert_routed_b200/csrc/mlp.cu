@@ -115,8 +115,8 @@ moe_status moe_mlp(const void *x, const uint32_t *ids, const float *weights, con
     const uint64_t few_to = !mid ? tmax<uint64_t>(64u, 4ull * num_experts)
                                  : tmax<uint64_t>(16u, narrow(gate_up) && narrow(down) ? num_experts : num_experts / 4u);
     if (path != MOE_PATH_GROUPED && (path == MOE_PATH_DECODE || R <= few_to) && mlp_few_supported(a))
-        return launch_mlp_few(a, (uint32_t *)ws, h, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
-    if (mid) return launch_mlp_mid(a, ws, ws + L.h, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+        return status_of(launch_mlp_few(a, (uint32_t *)ws, h, (cudaStream_t)stream));
+    if (mid) return status_of(launch_mlp_mid(a, ws, ws + L.h, (cudaStream_t)stream));
     const moe_dtype hd = h_dtype((int)x_dtype, (int)out_dtype);
     LayerProduct layer{0u};
     v = run_product(x, ids, *gate_up, h, m, hidden, 2u * inter, n_expert_used, num_experts, x_dtype, hd, (int)act,
@@ -127,10 +127,8 @@ moe_status moe_mlp(const void *x, const uint32_t *ids, const float *weights, con
     v = run_product(h, ids, *down, z, R, inter, hidden, 1, num_experts, hd, MOE_F32, -1, workspace, L.own, stream, path,
                     &layer);
     if (v != MOE_OK) return v;
-    return launch_combine(z, weights, ids, residual, out, m, n_expert_used, hidden, num_experts, DT_F32,
-                          (int)out_dtype, (cudaStream_t)stream) == cudaSuccess
-               ? MOE_OK
-               : MOE_ERR_CUDA;
+    return status_of(launch_combine(z, weights, ids, residual, out, m, n_expert_used, hidden, num_experts, DT_F32,
+                                    (int)out_dtype, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -68,12 +68,14 @@ unsigned long long current_context_id() {
 // the one the cached address came from), with that device current.
 moe_status scratch_address(void **out) {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
+    const cudaError_t ce = cudaGetDevice(&dev);
+    if (ce != cudaSuccess || dev < 0 || dev >= 64) return moe::status_of(ce == cudaSuccess ? cudaErrorInvalidDevice : ce);
     std::lock_guard<std::mutex> lock(g_scratch_mutex);
     const unsigned long long id = current_context_id();
     if (!g_scratch[dev].ptr || id == 0 || id != g_scratch[dev].ctx_id) {
         void *ptr = nullptr;
-        if (cudaGetSymbolAddress(&ptr, g_noalloc_scratch) != cudaSuccess || !ptr) return MOE_ERR_CUDA;
+        const cudaError_t e = cudaGetSymbolAddress(&ptr, g_noalloc_scratch);
+        if (e != cudaSuccess || !ptr) return moe::status_of(e == cudaSuccess ? cudaErrorInvalidSymbol : e);
         g_scratch[dev].ptr = ptr;
         g_scratch[dev].ctx_id = current_context_id();  // the lookup may have created the context
     }
